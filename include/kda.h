@@ -437,6 +437,178 @@ kda_status kda_output_gate_rmsnorm(const void *o, const void *z, const float *we
                                    cudaStream_t stream);
 
 /*
+ * kda_decode_step_opt over a pool of states: row n's state is slot slots[n] of
+ * `state`, [num_slots][H][dk][dv] fp32, read and updated in place; every other
+ * slot is left as it was.
+ *  slots      int32 [N] device array (4-byte aligned). Rows whose slot lies
+ *             outside [0, num_slots) (-1 by custom: the padding of a batch of
+ *             fixed size) touch no state and get zeros in `out`. Slots in
+ *             range must be distinct: two rows of one slot would race for its
+ *             state, whose contents (and those rows' outputs) are then
+ *             unspecified; nothing outside the slot is touched.
+ *  num_slots  >= 1
+ * Other arguments, results and errors as kda_decode_step_opt.
+ */
+kda_status kda_decode_step_slots(const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, float scale, float *state,
+                                 const int32_t *slots, void *out, int N, int num_slots, int H,
+                                 int dk, int dv, kda_dtype dtype, const kda_options *options,
+                                 cudaStream_t stream);
+
+/*
+ * The gated linear recurrence (the elementwise counterpart of the scan above:
+ * a vector state, one decay per channel, no keys):
+ *
+ *     h_t = a_t o h_{t-1} + w_t o x_t
+ *
+ * with a_t from g_t under kda_gate and the input weight w_t under kda_write.
+ * The sequences, their states and the gates follow kda_chunk_fwd.
+ */
+typedef enum {
+    KDA_WRITE_PLAIN = 0,      /* w = 1 */
+    KDA_WRITE_COMPLEMENT = 1, /* w = 1 - a: h_t lies between h_{t-1} and x_t */
+    KDA_WRITE_NORM = 2        /* w = sqrt(1 - a^2): keeps the variance of independent inputs */
+} kda_write;
+
+/*
+ * Options of the gated scan. A NULL pointer means {KDA_GATE_LOG, 0,
+ * KDA_WRITE_PLAIN}. gate_lower as in kda_options (KDA_GATE_BOUNDED only).
+ */
+typedef struct {
+    kda_gate gate;
+    float gate_lower;
+    kda_write write;
+} kda_scan_options;
+
+/* Tokens between the states that kda_gated_scan_fwd saves for the backward pass. */
+#define KDA_SCAN_CARRY_TOKENS 128
+
+/*
+ * Bytes of the `carries` array for these sizes: one row of D fp32 for each of
+ * floor(B T / KDA_SCAN_CARRY_TOKENS) + num_seqs carries. 0 for invalid sizes.
+ */
+size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs);
+
+/*
+ * The recurrence over whole sequences.
+ *  x          [tokens][D], dtype        inputs
+ *  g          [tokens][D], g_dtype      gate values (kda_gate). With
+ *             KDA_GATE_LOG: log a <= 0, -inf allowed (a = 0: a restart)
+ *  init_state [num_seqs][D] fp32, or NULL for zero initial states
+ *  cu_seqlens int32 [num_seqs + 1] device array or NULL, as kda_chunk_fwd.
+ *             Its contents are not read on the host; each offset is clamped to
+ *             [0, T] before use. Rows outside every sequence are left as they
+ *             were.
+ *  out        [tokens][D], dtype        h_t (written)
+ *  final_state[num_seqs][D] fp32 (written), or NULL. May alias init_state
+ *             exactly. A zero-length sequence's is its initial state.
+ *  carries    NULL, or kda_gated_scan_carries_size(...) bytes (written): the
+ *             fp32 state entering every KDA_SCAN_CARRY_TOKENS-th token of each
+ *             sequence, for kda_gated_scan_bwd. The state entering token
+ *             128 i of sequence n, which begins at token s, is row
+ *             floor(s / 128) + n + i; other rows are left as they were.
+ *  dtype, g_dtype: (BF16, BF16), (BF16, F32) or (F32, F32); (F32, BF16)
+ *             returns KDA_ERR_UNSUPPORTED
+ *  D          channels; a multiple of 4, else KDA_ERR_UNSUPPORTED
+ * Pointers 16-byte aligned (cu_seqlens 4-byte). No workspace. States and sums
+ * are fp32; the results do not depend on the run (no atomics).
+ */
+kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_state,
+                              const int32_t *cu_seqlens, void *out, float *final_state,
+                              float *carries, int B, int T, int D, int num_seqs, kda_dtype dtype,
+                              kda_dtype g_dtype, const kda_scan_options *options,
+                              cudaStream_t stream);
+
+/*
+ * The gradient of kda_gated_scan_fwd. With e_t the gradient with respect to
+ * h_t, taken from the last token to the first,
+ *
+ *     e_t = dout_t + a_{t+1} o e_{t+1}    (dfinal_state enters at the last token),
+ *     dx_t = w_t o e_t,   dinit = a_1 o e_1,
+ *     dg_t = (dlog a/dg) o e_t o (a_t o h_{t-1} + (dw/dlog a) o x_t).
+ *
+ * h_{t-1} is formed again from x, g and the saved `carries`.
+ *  dout       [tokens][D], dtype       gradient of out
+ *  dfinal_state [num_seqs][D] fp32, or NULL for zero
+ *  x, g, carries, cu_seqlens, sizes and options: those of the forward call
+ *  dx         [tokens][D], dtype (written)
+ *  dg         [tokens][D], g_dtype (written)
+ *  dinit_state [num_seqs][D] fp32 (written), or NULL. May alias dfinal_state
+ *             exactly. A zero-length sequence's is its dfinal_state (or zero).
+ * With KDA_WRITE_NORM the slope of w at a = 1 (log a = 0) is unbounded; where
+ * w is exactly 0 it is taken as 0. Alignment and errors as the forward call.
+ */
+kda_status kda_gated_scan_bwd(const void *dout, const float *dfinal_state, const void *x,
+                              const void *g, const float *carries, const int32_t *cu_seqlens,
+                              void *dx, void *dg, float *dinit_state, int B, int T, int D,
+                              int num_seqs, kda_dtype dtype, kda_dtype g_dtype,
+                              const kda_scan_options *options, cudaStream_t stream);
+
+/*
+ * One step of the recurrence for N rows, states updated in place.
+ *  x, g, out  [N][D] (dtype, g_dtype, dtype)
+ *  state      [num_slots][D] fp32
+ *  slots      int32 [N] device array, or NULL (then row n's state is slot n
+ *             and num_slots must be N); as in kda_decode_step_slots
+ */
+kda_status kda_gated_scan_step(const void *x, const void *g, float *state, const int32_t *slots,
+                               void *out, int N, int num_slots, int D, kda_dtype dtype,
+                               kda_dtype g_dtype, const kda_scan_options *options,
+                               cudaStream_t stream);
+
+/* Most entries of one kda_state_copy call. */
+#define KDA_STATE_COPY_MAX 4096
+
+/*
+ * Copies, forks, reorders and clears the slots of a pool of recurrent states:
+ * for i < n
+ *
+ *     pool[layer][dst[i]] = src[i] < 0 ? 0 : source[layer][src[i]]
+ *
+ * in every layer, as ONE parallel assignment: all sources are read before any
+ * slot is written, so a source may be another entry's destination (a swap, a
+ * beam search's reorder). Where entries name the same destination, the last
+ * one holds.
+ *  source     [layers][source_slots][slot_bytes], or NULL: the pool itself
+ *             (source_slots is then ignored). A source that is not NULL must
+ *             not overlap the pool.
+ *  pool       [layers][num_slots][slot_bytes] (written)
+ *  src, dst   int32 [n] device arrays (4-byte aligned). Entries whose dst lies
+ *             outside [0, num_slots) (-1 by custom), or whose src is not below
+ *             the source's slots, are skipped.
+ *  n          0 .. KDA_STATE_COPY_MAX, else KDA_ERR_UNSUPPORTED
+ *  layers     >= 1; slot_bytes a positive multiple of 16 (64 KiB per head for a
+ *             128 x 128 state)
+ * source and pool 16-byte aligned. No workspace; one launch.
+ */
+kda_status kda_state_copy(const void *source, int source_slots, void *pool, int num_slots,
+                          const int32_t *src, const int32_t *dst, int n, int layers,
+                          size_t slot_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace kda_state_compact needs (0 for num_slots <= 0). */
+size_t kda_state_compact_workspace_size(int num_slots);
+
+/*
+ * Moves a pool's live slots together: with n of num_slots slots live, the k-th
+ * live slot at or above n is copied into the k-th slot below n that is not
+ * live, in every layer, so that slots [0, n) are the live ones (a dense batch
+ * for kda_decode_step). No other slot is written: slots from n on keep what
+ * they held.
+ *  pool       [layers][num_slots][slot_bytes]
+ *  live       uint8 [num_slots], nonzero: live (read only)
+ *  new_slot   int32 [num_slots] (written): where each slot's state now is, -1
+ *             for a slot that was not live
+ *  count      int32 [1] (written): n
+ *  workspace  kda_state_compact_workspace_size(num_slots) bytes, 256-byte
+ *             aligned; contents on entry are ignored
+ * pool 16-byte aligned, new_slot and count 4-byte; layers and slot_bytes as
+ * kda_state_copy.
+ */
+kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live, int32_t *new_slot,
+                             int32_t *count, int layers, size_t slot_bytes, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Diagnostic of the failure detection (no counterpart on the pages): launches
  * one CTA that waits, with the kernels' bounded mbarrier wait limited to
  * `limit` polls (1 .. 4194304), on a barrier nothing ever completes; when the

@@ -16,12 +16,20 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 DECAY = {"channel": 0, "scalar": 1, "none": 2}           # kda_decay
 GATE = {"log": 0, "logsigmoid": 1, "bounded": 2}          # kda_gate
+WRITE = {"plain": 0, "complement": 1, "norm": 2}          # kda_write
+SCAN_CARRY_TOKENS = 128                                   # KDA_SCAN_CARRY_TOKENS
+STATE_COPY_MAX = 4096                                     # KDA_STATE_COPY_MAX
 
 
 class Options(ctypes.Structure):
     """kda_options of include/kda.h."""
     _fields_ = [("decay", ctypes.c_int), ("gate", ctypes.c_int), ("gate_lower", ctypes.c_float),
                 ("l2norm_qk", ctypes.c_int), ("segments", ctypes.c_int), ("fused", ctypes.c_int)]
+
+
+class ScanOptions(ctypes.Structure):
+    """kda_scan_options of include/kda.h."""
+    _fields_ = [("gate", ctypes.c_int), ("gate_lower", ctypes.c_float), ("write", ctypes.c_int)]
 
 
 _vp = ctypes.c_void_p
@@ -51,6 +59,17 @@ _SIGNATURES = {
                           + [ctypes.c_int] * 7 + [_vp, _vp, ctypes.c_size_t, _vp, _vp], ctypes.c_int),
     "kda_decode_step_opt": ([_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp]
                             + [ctypes.c_int] * 5 + [_vp, _vp], ctypes.c_int),
+    "kda_decode_step_slots": ([_vp, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp]
+                              + [ctypes.c_int] * 6 + [_vp, _vp], ctypes.c_int),
+    "kda_gated_scan_carries_size": ([ctypes.c_int] * 4, ctypes.c_size_t),
+    "kda_gated_scan_fwd": ([_vp] * 7 + [ctypes.c_int] * 6 + [_vp, _vp], ctypes.c_int),
+    "kda_gated_scan_bwd": ([_vp] * 9 + [ctypes.c_int] * 6 + [_vp, _vp], ctypes.c_int),
+    "kda_gated_scan_step": ([_vp] * 5 + [ctypes.c_int] * 5 + [_vp, _vp], ctypes.c_int),
+    "kda_state_copy": ([_vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int,
+                        ctypes.c_size_t, _vp], ctypes.c_int),
+    "kda_state_compact_workspace_size": ([ctypes.c_int], ctypes.c_size_t),
+    "kda_state_compact": ([_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, ctypes.c_size_t, _vp,
+                           ctypes.c_size_t, _vp], ctypes.c_int),
     "kda_selftest_wait_timeout": ([_vp, ctypes.c_uint, _vp], ctypes.c_int),
     "kda_output_gate_rmsnorm": ([_vp, _vp, _vp, ctypes.c_float, _vp, ctypes.c_longlong,
                                  ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp], ctypes.c_int),

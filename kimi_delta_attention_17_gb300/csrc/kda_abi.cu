@@ -3,7 +3,7 @@
 // happens here, on the host, before any CUDA call.
 #include <math.h>
 
-#include "kda_internal.cuh"
+#include "kda_scan.cuh"
 
 namespace kda {
 namespace {
@@ -141,6 +141,7 @@ chunk_table_kernel(const int32_t *__restrict__ cu_seqlens, int num_seqs, int T_f
     }
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool dims_ok(int dk, int dv) { return dk == dv && (dk == 64 || dk == 128); }
@@ -371,9 +372,9 @@ extern "C" kda_status kda_chunk_fwd_gated(const void *q, const void *k, const vo
 namespace {
 
 kda_status decode_impl(const void *q, const void *k, const void *v, const float *g,
-                       const float *beta, float scale, float *state, void *out, int N, int H,
-                       int dk, int dv, kda_dtype dtype, const kda_options *options,
-                       cudaStream_t stream) {
+                       const float *beta, float scale, float *state, const int32_t *slots,
+                       int num_slots, void *out, int N, int H, int dk, int dv, kda_dtype dtype,
+                       const kda_options *options, cudaStream_t stream) {
     Prologue pro;
     if (!make_prologue(options, &pro)) return KDA_ERR_INVALID_ARGUMENT;
     if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARGUMENT;
@@ -387,7 +388,7 @@ kda_status decode_impl(const void *q, const void *k, const void *v, const float 
     if ((reinterpret_cast<uintptr_t>(beta) & 3u) != 0) return KDA_ERR_INVALID_ARGUMENT;
     if (!dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
     const cudaError_t err =
-        launch_decode(q, k, v, g, beta, scale, state, out, N, H, dk, dtype, pro, stream);
+        launch_decode(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, dk, dtype, pro, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -397,7 +398,8 @@ extern "C" kda_status kda_decode_step(const void *q, const void *k, const void *
                                       const float *beta, float scale, float *state, void *out,
                                       int N, int H, int dk, int dv, kda_dtype dtype,
                                       cudaStream_t stream) {
-    return decode_impl(q, k, v, g, beta, scale, state, out, N, H, dk, dv, dtype, nullptr, stream);
+    return decode_impl(q, k, v, g, beta, scale, state, nullptr, N, out, N, H, dk, dv, dtype, nullptr,
+                       stream);
 }
 
 extern "C" kda_status kda_decode_step_opt(const void *q, const void *k, const void *v,
@@ -405,7 +407,184 @@ extern "C" kda_status kda_decode_step_opt(const void *q, const void *k, const vo
                                           float *state, void *out, int N, int H, int dk, int dv,
                                           kda_dtype dtype, const kda_options *options,
                                           cudaStream_t stream) {
-    return decode_impl(q, k, v, g, beta, scale, state, out, N, H, dk, dv, dtype, options, stream);
+    return decode_impl(q, k, v, g, beta, scale, state, nullptr, N, out, N, H, dk, dv, dtype, options,
+                       stream);
+}
+
+extern "C" kda_status kda_decode_step_slots(const void *q, const void *k, const void *v,
+                                            const float *g, const float *beta, float scale,
+                                            float *state, const int32_t *slots, void *out, int N,
+                                            int num_slots, int H, int dk, int dv, kda_dtype dtype,
+                                            const kda_options *options, cudaStream_t stream) {
+    if (num_slots <= 0 || (N > 0 && !slots)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(slots)) return KDA_ERR_INVALID_ARGUMENT;
+    if (H > 0 && (long long)num_slots * H >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
+    return decode_impl(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, dk, dv, dtype,
+                       options, stream);
+}
+
+namespace {
+
+// kda_scan_options, and the storage types, as the kernels take them.
+kda_status make_scan_gate(const kda_scan_options *o, kda_dtype dtype, kda_dtype g_dtype, ScanGate *gate) {
+    *gate = ScanGate{KDA_GATE_LOG, KDA_WRITE_PLAIN, 0.f};
+    if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARGUMENT;
+    if (g_dtype != KDA_DTYPE_F32 && g_dtype != KDA_DTYPE_BF16) return KDA_ERR_INVALID_ARGUMENT;
+    if (o) {
+        if (o->gate != KDA_GATE_LOG && o->gate != KDA_GATE_LOGSIGMOID && o->gate != KDA_GATE_BOUNDED)
+            return KDA_ERR_INVALID_ARGUMENT;
+        if (o->gate == KDA_GATE_BOUNDED && !(o->gate_lower >= -10.f && o->gate_lower < 0.f))
+            return KDA_ERR_INVALID_ARGUMENT;
+        if (o->write != KDA_WRITE_PLAIN && o->write != KDA_WRITE_COMPLEMENT && o->write != KDA_WRITE_NORM)
+            return KDA_ERR_INVALID_ARGUMENT;
+        *gate = ScanGate{(int)o->gate, (int)o->write, o->gate == KDA_GATE_BOUNDED ? o->gate_lower : 0.f};
+    }
+    return KDA_OK;
+}
+
+// The checks that the scan's forward and backward calls share.
+kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options) {
+    const kda_status st = make_scan_gate(options, s->dtype, s->g_dtype, &s->gate);
+    if (st != KDA_OK) return st;
+    if (B <= 0 || T < 0 || s->D <= 0 || s->num_seqs <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (s->cu ? B != 1 : s->num_seqs != B) return KDA_ERR_INVALID_ARGUMENT;
+    s->tokens = (long long)B * T;
+    s->T_fixed = T;
+    if (s->tokens >= (1LL << 31) - kChunk) return KDA_ERR_INVALID_ARGUMENT;
+    if (s->tokens * s->D >= (1LL << 40)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)s->num_seqs * ((s->D + 31) / 32) * 8 >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
+    if (s->tokens > 0 && (!s->x || !s->g)) return KDA_ERR_INVALID_ARGUMENT;
+    const void *tensors[] = {s->x,  s->g,  s->dout,        s->init,  s->dfinal, s->out,
+                             s->dx, s->dg, s->final_state, s->dinit, s->carries};
+    for (const void *p : tensors)
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(s->cu)) return KDA_ERR_INVALID_ARGUMENT;
+    if (s->D % kScanVec != 0) return KDA_ERR_UNSUPPORTED;
+    if (s->dtype == KDA_DTYPE_F32 && s->g_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs) {
+    if (B <= 0 || T < 0 || D <= 0 || num_seqs <= 0) return 0;
+    if (num_seqs != B && B != 1) return 0;
+    return (size_t)((long long)B * T / KDA_SCAN_CARRY_TOKENS + num_seqs) * (size_t)D * sizeof(float);
+}
+
+extern "C" kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_state,
+                                         const int32_t *cu_seqlens, void *out, float *final_state,
+                                         float *carries, int B, int T, int D, int num_seqs,
+                                         kda_dtype dtype, kda_dtype g_dtype,
+                                         const kda_scan_options *options, cudaStream_t stream) {
+    ScanArgs s = {};
+    s.x = x;
+    s.g = g;
+    s.init = init_state;
+    s.cu = cu_seqlens;
+    s.out = out;
+    s.final_state = final_state;
+    s.carries = carries;
+    s.D = D;
+    s.num_seqs = num_seqs;
+    s.dtype = dtype;
+    s.g_dtype = g_dtype;
+    const kda_status st = scan_check(&s, B, T, options);
+    if (st != KDA_OK) return st;
+    if (s.tokens > 0 && !out) return KDA_ERR_INVALID_ARGUMENT;
+    return launch_scan_fwd(s, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_gated_scan_bwd(const void *dout, const float *dfinal_state, const void *x,
+                                         const void *g, const float *carries,
+                                         const int32_t *cu_seqlens, void *dx, void *dg,
+                                         float *dinit_state, int B, int T, int D, int num_seqs,
+                                         kda_dtype dtype, kda_dtype g_dtype,
+                                         const kda_scan_options *options, cudaStream_t stream) {
+    ScanArgs s = {};
+    s.x = x;
+    s.g = g;
+    s.dout = dout;
+    s.dfinal = dfinal_state;
+    s.cu = cu_seqlens;
+    s.dx = dx;
+    s.dg = dg;
+    s.dinit = dinit_state;
+    s.carries = const_cast<float *>(carries);
+    s.D = D;
+    s.num_seqs = num_seqs;
+    s.dtype = dtype;
+    s.g_dtype = g_dtype;
+    const kda_status st = scan_check(&s, B, T, options);
+    if (st != KDA_OK) return st;
+    if (s.tokens > 0 && (!dout || !carries || !dx || !dg)) return KDA_ERR_INVALID_ARGUMENT;
+    return launch_scan_bwd(s, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_gated_scan_step(const void *x, const void *g, float *state,
+                                          const int32_t *slots, void *out, int N, int num_slots,
+                                          int D, kda_dtype dtype, kda_dtype g_dtype,
+                                          const kda_scan_options *options, cudaStream_t stream) {
+    ScanStepArgs s = {x, g, state, slots, out, N, num_slots, D, dtype, g_dtype, ScanGate{}};
+    const kda_status st = make_scan_gate(options, dtype, g_dtype, &s.gate);
+    if (st != KDA_OK) return st;
+    if (N < 0 || D <= 0 || (slots ? num_slots <= 0 : num_slots != N)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)N * D >= (1LL << 37)) return KDA_ERR_INVALID_ARGUMENT;  // grid of 512-channel blocks
+    if (N > 0 && (!x || !g || !state || !out)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(x) || !aligned16(g) || !aligned16(state) || !aligned16(out) || !aligned4(slots))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (D % kScanVec != 0) return KDA_ERR_UNSUPPORTED;
+    if (dtype == KDA_DTYPE_F32 && g_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
+    return launch_scan_step(s, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+namespace {
+
+// A pool's sizes: whole 16-byte pieces, and a size that byte offsets can hold.
+constexpr size_t kPoolMost = (size_t)1 << 46;
+bool pool_ok(int num_slots, int layers, size_t slot_bytes) {
+    if (num_slots <= 0 || layers <= 0 || slot_bytes == 0 || slot_bytes % 16 != 0) return false;
+    return slot_bytes <= kPoolMost && (size_t)num_slots * (size_t)layers <= kPoolMost / slot_bytes;
+}
+
+}  // namespace
+
+extern "C" kda_status kda_state_copy(const void *source, int source_slots, void *pool,
+                                     int num_slots, const int32_t *src, const int32_t *dst, int n,
+                                     int layers, size_t slot_bytes, cudaStream_t stream) {
+    if (!pool_ok(num_slots, layers, slot_bytes) || n < 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (!pool || (n > 0 && (!src || !dst))) return KDA_ERR_INVALID_ARGUMENT;
+    if (source && !pool_ok(source_slots, layers, slot_bytes)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(pool) || !aligned16(source) || !aligned4(src) || !aligned4(dst))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (source) {
+        // A source inside the pool would be read and written at once.
+        const uintptr_t s0 = reinterpret_cast<uintptr_t>(source), p0 = reinterpret_cast<uintptr_t>(pool);
+        const size_t bytes = slot_bytes * layers;
+        if (s0 < p0 + bytes * num_slots && p0 < s0 + bytes * source_slots) return KDA_ERR_INVALID_ARGUMENT;
+    }
+    if (n > KDA_STATE_COPY_MAX) return KDA_ERR_UNSUPPORTED;
+    const cudaError_t err =
+        launch_state_copy(source, source_slots, pool, num_slots, src, dst, n, layers, slot_bytes, stream);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" size_t kda_state_compact_workspace_size(int num_slots) {
+    return num_slots > 0 ? compact_workspace(num_slots) : 0;
+}
+
+extern "C" kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live,
+                                        int32_t *new_slot, int32_t *count, int layers,
+                                        size_t slot_bytes, void *workspace, size_t workspace_bytes,
+                                        cudaStream_t stream) {
+    if (!pool_ok(num_slots, layers, slot_bytes)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!pool || !live || !new_slot || !count) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(pool) || !aligned4(new_slot) || !aligned4(count)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!workspace || workspace_bytes < compact_workspace(num_slots)) return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
+    const cudaError_t err = launch_state_compact(pool, num_slots, live, new_slot, count, layers, slot_bytes,
+                                                 workspace, stream);
+    return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status kda_output_gate_rmsnorm(const void *o, const void *z, const float *weight,

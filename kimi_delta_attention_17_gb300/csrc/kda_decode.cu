@@ -26,11 +26,15 @@ constexpr int kSlab = 32;  // state columns per CTA
 // gate logits through the log-sigmoid, q and k normalised), each compiled
 // with its options fixed; 1 takes every option at run time.
 constexpr int kDecPlain = 0, kDecRuntime = 1, kDecGated = 2;
-template <int D, typename InT, int kVar>
+// kSlots: the state is a pool, and row n's is slot slots[n] (a row out of
+// range writes zeros and touches no state); compiled apart so that the dense
+// step keeps its code.
+template <int D, typename InT, int kVar, bool kSlots>
 __global__ void __launch_bounds__(kDecodeThreads, 7)
 decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT *__restrict__ v,
                    const float *__restrict__ g, const float *__restrict__ beta, float scale,
-                   float *__restrict__ state, InT *__restrict__ out, Prologue pro) {
+                   float *__restrict__ state, const int32_t *__restrict__ slots, int num_slots, int H,
+                   InT *__restrict__ out, Prologue pro) {
     constexpr bool kOpts = kVar != kDecPlain;
     if (kVar == kDecGated) pro = Prologue{KDA_DECAY_CHANNEL, KDA_GATE_LOGSIGMOID, 0.f, 1};
     constexpr int R = D / 16;  // rows per thread
@@ -40,7 +44,19 @@ decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const I
     const int cq = tid & 7;   // column quad within the slab
     const int rg = tid >> 3;  // row group 0..15; rows rg + 16 m
 
-    float *S = state + (size_t)nh * D * D + col0 + 4 * cq;
+    size_t at = nh;  // the state's place in units of d x d
+    if (kSlots) {
+        const int n = nh / H, slot = slots[n];
+        if (slot < 0 || slot >= num_slots) {
+            if (rg == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[(size_t)nh * D + col0 + 4 * cq + i] = from_f32<InT>(0.f);
+            }
+            return;
+        }
+        at = (size_t)slot * H + (nh - n * H);
+    }
+    float *S = state + at * D * D + col0 + 4 * cq;
     float4 s[R];
 #pragma unroll
     for (int m = 0; m < R; ++m)
@@ -160,19 +176,20 @@ decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const I
     }
 }
 
-template <int D, typename InT>
+template <int D, typename InT, bool kSlots>
 cudaError_t launch_decode_t(const void *q, const void *k, const void *v, const float *g,
-                            const float *beta, float scale, float *state, void *out, int N, int H,
-                            const Prologue &pro, cudaStream_t stream) {
+                            const float *beta, float scale, float *state, const int32_t *slots,
+                            int num_slots, void *out, int N, int H, const Prologue &pro,
+                            cudaStream_t stream) {
     dim3 grid((unsigned)(N * H), D / kSlab);
     const bool chan = pro.decay == KDA_DECAY_CHANNEL;
     const int var = chan && pro.gate == KDA_GATE_LOG && !pro.l2norm              ? kDecPlain
                     : chan && pro.gate == KDA_GATE_LOGSIGMOID && pro.l2norm ? kDecGated
                                                                                : kDecRuntime;
 #define KDA_DECODE_LAUNCH(V)                                                                   \
-    decode_step_kernel<D, InT, V><<<grid, kDecodeThreads, 0, stream>>>(                          \
+    decode_step_kernel<D, InT, V, kSlots><<<grid, kDecodeThreads, 0, stream>>>(                          \
         static_cast<const InT *>(q), static_cast<const InT *>(k), static_cast<const InT *>(v), g, \
-        beta, scale, state, static_cast<InT *>(out), pro)
+        beta, scale, state, slots, num_slots, H, static_cast<InT *>(out), pro)
     switch (var) {
         case kDecPlain: KDA_DECODE_LAUNCH(kDecPlain); break;
         case kDecGated: KDA_DECODE_LAUNCH(kDecGated); break;
@@ -182,18 +199,28 @@ cudaError_t launch_decode_t(const void *q, const void *k, const void *v, const f
     return cudaGetLastError();
 }
 
+template <int D, typename InT>
+cudaError_t launch_decode_s(const void *q, const void *k, const void *v, const float *g,
+                            const float *beta, float scale, float *state, const int32_t *slots,
+                            int num_slots, void *out, int N, int H, const Prologue &pro,
+                            cudaStream_t stream) {
+    return slots ? launch_decode_t<D, InT, true>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream)
+                 : launch_decode_t<D, InT, false>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_decode(const void *q, const void *k, const void *v, const float *g,
-                          const float *beta, float scale, float *state, void *out, int N, int H,
-                          int d, kda_dtype dtype, const Prologue &pro, cudaStream_t stream) {
+                          const float *beta, float scale, float *state, const int32_t *slots,
+                          int num_slots, void *out, int N, int H, int d, kda_dtype dtype,
+                          const Prologue &pro, cudaStream_t stream) {
     if (N == 0) return cudaSuccess;
     if (dtype == KDA_DTYPE_BF16) {
-        return d == 128 ? launch_decode_t<128, __nv_bfloat16>(q, k, v, g, beta, scale, state, out, N, H, pro, stream)
-                        : launch_decode_t<64, __nv_bfloat16>(q, k, v, g, beta, scale, state, out, N, H, pro, stream);
+        return d == 128 ? launch_decode_s<128, __nv_bfloat16>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream)
+                        : launch_decode_s<64, __nv_bfloat16>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream);
     }
-    return d == 128 ? launch_decode_t<128, float>(q, k, v, g, beta, scale, state, out, N, H, pro, stream)
-                    : launch_decode_t<64, float>(q, k, v, g, beta, scale, state, out, N, H, pro, stream);
+    return d == 128 ? launch_decode_s<128, float>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream)
+                    : launch_decode_s<64, float>(q, k, v, g, beta, scale, state, slots, num_slots, out, N, H, pro, stream);
 }
 
 }  // namespace kda

@@ -166,9 +166,19 @@ cudaError_t launch_output_gate_rmsnorm(const void *o, const void *z, const float
                                        void *out, long long rows, int dv, kda_dtype dtype,
                                        cudaStream_t stream);
 
-// Decode step.
+// Decode step; row n's state is slot slots[n] of num_slots, or n where slots is NULL.
 cudaError_t launch_decode(const void *q, const void *k, const void *v, const float *g,
-                          const float *beta, float scale, float *state, void *out, int N, int H,
-                          int d, kda_dtype dtype, const Prologue &pro, cudaStream_t stream);
+                          const float *beta, float scale, float *state, const int32_t *slots,
+                          int num_slots, void *out, int N, int H, int d, kda_dtype dtype,
+                          const Prologue &pro, cudaStream_t stream);
+
+// State pool (checked arguments).
+cudaError_t launch_state_copy(const void *source, int source_slots, void *pool, int num_slots,
+                              const int32_t *src, const int32_t *dst, int n, int layers,
+                              size_t slot_bytes, cudaStream_t stream);
+size_t compact_workspace(int num_slots);
+cudaError_t launch_state_compact(void *pool, int num_slots, const uint8_t *live, int32_t *new_slot,
+                                 int32_t *count, int layers, size_t slot_bytes, void *workspace,
+                                 cudaStream_t stream);
 
 }  // namespace kda

@@ -2,6 +2,7 @@
 torch CUDA tensors. It only marshals arguments (pointers, sizes, the current
 stream) and allocates outputs and scratch with torch when the caller does not
 pass them; every step of the computation runs in the library's kernels."""
+import contextlib
 import ctypes
 
 import torch
@@ -156,12 +157,34 @@ def chunk_fwd(q, k, v, g, beta, scale, init_state=None, cu_seqlens=None, *, out=
     return out, final_state
 
 
+def _scope(device, stream):
+    """Context in which allocations and launches of a call on ``device``'s
+    tensors belong to its stream (the device's current one when None)."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("stream must belong to the tensors' device")
+        return torch.cuda.stream(stream)
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError("%s must be on the same device as the other tensors" % name)
+
+
 def decode_step(q, k, v, g, beta, scale, state, *, out=None, stream=None, decay="channel",
-                gate="log", gate_lower=-5.0, l2norm_qk=False):
+                gate="log", gate_lower=-5.0, l2norm_qk=False, slots=None):
     """One decode step, state updated in place. q, k [N, H, dk]; v [N, H, dv];
     g [N, H, dk] fp32; beta [N, H] fp32; state [N, H, dk, dv] fp32.
     Returns out [N, H, dv]. Options as in chunk_fwd (with "scalar" decay g is
-    [N, H]; kda_decode_step_opt)."""
+    [N, H]; kda_decode_step_opt).
+    ``slots`` (int32 [N], on the device): ``state`` is a pool [P, H, dk, dv] and
+    row n's state its slot slots[n] (kda_decode_step_slots). Rows whose slot
+    lies outside [0, P) (-1: padding) touch no state and get zeros; slots in
+    range must be distinct."""
     _need(q, "q", ndim=3)
     dtype = q.dtype
     if dtype not in _DTYPES:
@@ -173,6 +196,9 @@ def decode_step(q, k, v, g, beta, scale, state, *, out=None, stream=None, decay=
     _need(state, "state", torch.float32, 4)
     N, H, dk = q.shape
     dv = v.shape[-1]
+    if slots is not None:
+        return _decode_step_slots(q, k, v, g, beta, scale, state, slots, out, stream,
+                                  _options(decay, gate, gate_lower, l2norm_qk), decay)
     if out is None:
         out = torch.empty((N, H, dv), dtype=dtype, device=q.device)
     else:
@@ -185,6 +211,36 @@ def decode_step(q, k, v, g, beta, scale, state, *, out=None, stream=None, decay=
     else:
         _lib.check("kda_decode_step_opt",
                    _lib.lib().kda_decode_step_opt(*head, ctypes.byref(opts), _stream_ptr(stream)))
+    return out
+
+
+def _decode_step_slots(q, k, v, g, beta, scale, state, slots, out, stream, opts, decay):
+    """decode_step over a pool; its tensors are checked for type, not yet for shape."""
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    _need(slots, "slots", torch.int32, 1)
+    if k.shape != q.shape or v.shape[:2] != q.shape[:2] or beta.shape != q.shape[:2]:
+        raise ValueError("q, k, v and beta must share [N, H]")
+    if decay != "none" and g.shape != (q.shape if decay == "channel" else q.shape[:2]):
+        raise ValueError("g must be [N, H, dk], or [N, H] with the scalar decay")
+    if slots.shape[0] != N:
+        raise ValueError("slots must have one entry per row")
+    if state.shape[1:] != (H, dk, dv):
+        raise ValueError("state must be [P, H, dk, dv]")
+    _same_device(q, k=k, v=v, g=g if decay != "none" else None, beta=beta, state=state, slots=slots,
+                 out=out)
+    with _scope(q.device, stream):
+        if out is None:
+            out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        else:
+            _need(out, "out", q.dtype, 3)
+            if out.shape != v.shape:
+                raise ValueError("out must have v's shape")
+        _lib.check("kda_decode_step_slots", _lib.lib().kda_decode_step_slots(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state), _ptr(slots),
+            _ptr(out), N, state.shape[0], H, dk, dv, _DTYPES[q.dtype],
+            None if opts is None else ctypes.byref(opts),
+            torch.cuda.current_stream(q.device).cuda_stream))
     return out
 
 

@@ -1,0 +1,176 @@
+"""Binding of the gated linear recurrence (kda_gated_scan_*): h_t = a_t h_{t-1}
++ w_t x_t per channel, over whole sequences with its gradient, and one token at
+a time. Only arguments are marshalled here."""
+import ctypes
+
+import torch
+
+from . import _lib
+from .kda import _DTYPES, _need, _ptr, _same_device, _scope
+
+
+def _scan_options(gate, gate_lower, write):
+    if gate not in _lib.GATE or write not in _lib.WRITE:
+        raise ValueError("gate must be one of %s and write one of %s"
+                         % (sorted(_lib.GATE), sorted(_lib.WRITE)))
+    return _lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write])
+
+
+def _tokens(x, g, cu_seqlens):
+    """Checks x [B, T, ...], g and cu_seqlens; returns B, T, D, num_seqs."""
+    _need(x, "x")
+    if x.dim() < 3:
+        raise ValueError("x must be [B, T, channels...]")
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32")
+    _need(g, "g")
+    if g.dtype not in _DTYPES:
+        raise ValueError("g must be bfloat16 or float32")
+    if g.shape != x.shape:
+        raise ValueError("g must have x's shape")
+    B, T = x.shape[:2]
+    D = 1
+    for n in x.shape[2:]:
+        D *= n
+    if cu_seqlens is None:
+        return B, T, D, B
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if B != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("packed sequences need B = 1 and cu_seqlens [N + 1]")
+    return B, T, D, cu_seqlens.numel() - 1
+
+
+def _states(t, name, N, x):
+    """A states tensor [N, channels...] fp32, or None."""
+    if t is not None:
+        _need(t, name, torch.float32)
+        if t.shape != (N,) + x.shape[2:]:
+            raise ValueError("%s must be [%d, %s]" % (name, N, ", ".join(map(str, x.shape[2:]))))
+    return t
+
+
+def _like(t, name, of, what):
+    if t is not None:
+        _need(t, name, of.dtype)
+        if t.shape != of.shape:
+            raise ValueError("%s must have %s's shape" % (name, what))
+    return t
+
+
+def _carry_rows(B, T, N):
+    return B * T // _lib.SCAN_CARRY_TOKENS + N
+
+
+def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_state=None,
+                   carries=None, save_carries=False, output_final_state=True, stream=None,
+                   gate="log", gate_lower=-5.0, write="plain"):
+    """The gated linear recurrence h_t = a_t h_{t-1} + w_t x_t, per channel, over
+    whole sequences (kda_gated_scan_fwd). x [B, T, channels...] (bf16 or fp32;
+    the channels in any number of dimensions, e.g. [B, T, H, d]); g of x's shape
+    (fp32, or bf16 with bf16 x); init_state [N, channels...] fp32 or None;
+    cu_seqlens int32 [N + 1] (device) or None (then N = B). The number of
+    channels must be a multiple of 4.
+    Returns (out, final_state or None, carries or None): out the states h_t in
+    x's type, final_state [N, channels...] fp32.
+    ``gate``: "log" (g is log a), "logsigmoid" (a = sigmoid(g)) or "bounded"
+    (log a = gate_lower * sigmoid(g)). ``write``: "plain" (w = 1), "complement"
+    (w = 1 - a) or "norm" (w = sqrt(1 - a^2)).
+    ``save_carries`` (or a ``carries`` buffer) keeps what gated_scan_bwd needs:
+    the fp32 state entering every 128th token, [B T // 128 + N, D].
+    Rows of ``out`` outside every sequence are left as they were."""
+    B, T, D, N = _tokens(x, g, cu_seqlens)
+    opts = _scan_options(gate, gate_lower, write)
+    _states(init_state, "init_state", N, x)
+    _states(final_state, "final_state", N, x)
+    _like(out, "out", x, "x")
+    rows = _carry_rows(B, T, N)
+    if carries is not None:
+        _need(carries, "carries", torch.float32, 2)
+        if carries.shape != (rows, D):
+            raise ValueError("carries must be [%d, %d]" % (rows, D))
+    _same_device(x, g=g, init_state=init_state, cu_seqlens=cu_seqlens, out=out,
+                 final_state=final_state, carries=carries)
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
+        if carries is None and save_carries:
+            carries = torch.empty((rows, D), dtype=torch.float32, device=x.device)
+        _lib.check("kda_gated_scan_fwd", _lib.lib().kda_gated_scan_fwd(
+            _ptr(x), _ptr(g), _ptr(init_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
+            _ptr(carries), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype], ctypes.byref(opts),
+            torch.cuda.current_stream(x.device).cuda_stream))
+    return out, final_state, carries
+
+
+def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, dx=None, dg=None,
+                   dinit_state=None, output_dinit_state=True, stream=None, gate="log",
+                   gate_lower=-5.0, write="plain"):
+    """The gradient of gated_scan_fwd (kda_gated_scan_bwd): dout of x's shape and
+    type, dfinal_state [N, channels...] fp32 or None; x, g, cu_seqlens and the
+    options of the forward call, and the ``carries`` that it saved.
+    Returns (dx, dg, dinit_state or None), in the types of x, g and fp32."""
+    B, T, D, N = _tokens(x, g, cu_seqlens)
+    opts = _scan_options(gate, gate_lower, write)
+    _like(dout, "dout", x, "x")
+    if dout is None:
+        raise TypeError("dout must be a torch.Tensor")
+    _need(carries, "carries", torch.float32, 2)
+    if carries.shape != (_carry_rows(B, T, N), D):
+        raise ValueError("carries must be [%d, %d]" % (_carry_rows(B, T, N), D))
+    _states(dfinal_state, "dfinal_state", N, x)
+    _states(dinit_state, "dinit_state", N, x)
+    _like(dx, "dx", x, "x")
+    _like(dg, "dg", g, "g")
+    _same_device(x, g=g, dout=dout, carries=carries, cu_seqlens=cu_seqlens,
+                 dfinal_state=dfinal_state, dinit_state=dinit_state, dx=dx, dg=dg)
+    with _scope(x.device, stream):
+        if dx is None:
+            dx = torch.empty_like(x)
+        if dg is None:
+            dg = torch.empty_like(g)
+        if dinit_state is None and output_dinit_state:
+            dinit_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
+        _lib.check("kda_gated_scan_bwd", _lib.lib().kda_gated_scan_bwd(
+            _ptr(dout), _ptr(dfinal_state), _ptr(x), _ptr(g), _ptr(carries), _ptr(cu_seqlens),
+            _ptr(dx), _ptr(dg), _ptr(dinit_state), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype],
+            ctypes.byref(opts), torch.cuda.current_stream(x.device).cuda_stream))
+    return dx, dg, dinit_state
+
+
+def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log", gate_lower=-5.0,
+                    write="plain"):
+    """One token of gated_scan_fwd for N rows, states updated in place
+    (kda_gated_scan_step): x, g [N, channels...]; state [N, channels...] fp32,
+    or with ``slots`` (int32 [N], on the device) a pool [P, channels...] whose
+    slot slots[n] is row n's state. Rows whose slot lies outside [0, P) (-1:
+    padding) touch no state and get zeros; slots in range must be distinct.
+    Returns out [N, channels...] in x's type. Options as in gated_scan_fwd."""
+    _need(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [N, channels...]")
+    _need(g, "g")
+    _, _, D, _ = _tokens(x.unsqueeze(0), g.unsqueeze(0), None)
+    opts = _scan_options(gate, gate_lower, write)
+    _need(state, "state", torch.float32)
+    N = x.shape[0]
+    if state.shape[1:] != x.shape[1:] or state.dim() != x.dim():
+        raise ValueError("state must be [slots, %s]" % ", ".join(map(str, x.shape[1:])))
+    if slots is None:
+        if state.shape[0] != N:
+            raise ValueError("state must have one row per row of x, or slots be given")
+    else:
+        _need(slots, "slots", torch.int32, 1)
+        if slots.shape[0] != N:
+            raise ValueError("slots must have one entry per row")
+    _like(out, "out", x, "x")
+    _same_device(x, g=g, state=state, slots=slots, out=out)
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        _lib.check("kda_gated_scan_step", _lib.lib().kda_gated_scan_step(
+            _ptr(x), _ptr(g), _ptr(state), _ptr(slots), _ptr(out), N, state.shape[0], D,
+            _DTYPES[x.dtype], _DTYPES[g.dtype], ctypes.byref(opts),
+            torch.cuda.current_stream(x.device).cuda_stream))
+    return out
