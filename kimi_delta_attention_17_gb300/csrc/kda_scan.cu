@@ -4,9 +4,9 @@
 // A step is the affine map h -> A h + H with (A, H) = (a_t, w_t x_t); maps
 // compose associatively, (A, H) then (A', H') being (A' A, A' H + H'), so time
 // is cut into pieces whose maps are formed side by side and then composed in
-// order. One thread holds kTpt consecutive tokens of four channels, a CTA 32
-// such pieces of 32 channels (8 lanes across, 4 pieces per warp, 8 warps), and
-// a cluster of CTAs consecutive tiles of the same channels. The thread maps
+// order. One thread holds 8 consecutive tokens of four channels, a CTA 16 such
+// pieces of 32 channels (8 lanes across, 4 pieces per warp, 4 warps), and a
+// cluster of CTAs consecutive tiles of the same channels. The thread maps
 // are composed by shuffles in the warp, through shared memory in the CTA and
 // through distributed shared memory in the cluster; every thread then knows
 // the state that enters its piece and walks it once more, from the a and w x
@@ -22,25 +22,17 @@
 namespace kda {
 namespace {
 
-constexpr int kLanes = 8;                          // threads across the channels
-constexpr int kBlockCh = kLanes * kScanVec;        // channels per CTA
-constexpr int kScanThreads = 256;
-constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kGroups = kScanThreads / kLanes;     // pieces of consecutive tokens per tile
-constexpr int kMaxCluster = 8;
-
 template <typename XT, typename GT>
 struct FwdShape {
-    static constexpr int kTpt = sizeof(XT) == 4 ? 4 : 8;  // tokens per thread
-    static constexpr int kTile = kGroups * kTpt;
     using XP = typename Piece<XT>::type;
     using GP = typename Piece<GT>::type;
-    static constexpr int kStages = 2;
-    static constexpr size_t smem = (size_t)kStages * kTpt * kScanThreads * (sizeof(XP) + sizeof(GP));
+    static constexpr size_t slots = (size_t)kScanStages * kScanTpt * kScanThreads;
+    static constexpr size_t smem = slots * (sizeof(XP) + sizeof(GP));
+    static constexpr int per_sm = smem <= 50 * 1024 ? 4 : 3;  // CTAs
 };
 
 template <typename XT, typename GT, int kGate, int kWrite>
-__global__ void __launch_bounds__(kScanThreads, 2)
+__global__ void __launch_bounds__(kScanThreads, FwdShape<XT, GT>::per_sm)
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
@@ -48,80 +40,92 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     using S = FwdShape<XT, GT>;
     using XP = typename S::XP;
     using GP = typename S::GP;
-    constexpr int kTpt = S::kTpt;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    XP *xs = reinterpret_cast<XP *>(smem_raw);
-    GP *gs = reinterpret_cast<GP *>(smem_raw + (size_t)S::kStages * kTpt * kScanThreads * sizeof(XP));
-    __shared__ __align__(16) float warp_map[2][kScanWarps][2][kBlockCh];
-    __shared__ __align__(16) float cta_map[2][kMaxCluster][2][kBlockCh];
+    GP *gs = reinterpret_cast<GP *>(smem_raw);
+    XP *xs = reinterpret_cast<XP *>(smem_raw + S::slots * sizeof(GP));
+    __shared__ __align__(16) float warp_map[2][kScanWarps][2][kScanCh];    // (A, H) of each warp
+    __shared__ __align__(16) float cta_map[2][kScanMaxRanks][2][kScanCh];  // and of each CTA
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
-    const long long unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
-    const int n = (int)(unit / blocks);
-    const int col = kScanVec * (lane & 7);
-    const int ch = (int)(unit % blocks) * kBlockCh + col;
+    const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
+    const int n = (int)(unit / (unsigned)blocks);
+    const int col = kScanVec * (lane & (kScanLanes - 1));
+    const int ch = (int)(unit % (unsigned)blocks) * kScanCh + col;
     const bool has_ch = ch < D;
-    const int group = tid / kLanes;
+    const int group = tid / kScanLanes;
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
-    const long long len = end - begin;
-    const long long super = (long long)S::kTile * ranks;  // tokens per cluster step
-    const long long steps = (len + super - 1) / super;
+    const int len = (int)(end - begin);
+    const int super = kScanTile * ranks;  // tokens per cluster step
+    const int steps = (int)(((long long)len + super - 1) / super);
 
     float carry[kScanVec] = {0.f, 0.f, 0.f, 0.f};
     if (init && has_ch) unpack4(*reinterpret_cast<const float4 *>(init + (size_t)n * D + ch), carry);
 
-    auto first_token = [&](long long i) { return (i * ranks + rank) * S::kTile + group * kTpt; };
-    auto prefetch = [&](long long i) {
-        const int st = (int)(i & 1);
-        const long long t = first_token(i);
-        if (has_ch && i < steps) {
-            const size_t at = (size_t)(begin + t) * D + ch;
+    // Tokens of this thread in step i that lie before the sequence's end.
+    auto tokens_left = [&](int i) {
+        const long long t = ((long long)i * ranks + rank) * kScanTile + group * kScanTpt;
+        return has_ch ? (int)min(max(len - t, 0LL), (long long)kScanTpt) : 0;
+    };
+    size_t at = (size_t)(begin + (long long)rank * kScanTile + group * kScanTpt) * D + ch;  // first element of a step
+    const size_t stride = (size_t)super * D;
+    auto prefetch = [&](int i, size_t from) {
+        const int left = i < steps ? tokens_left(i) : 0;
+        const int s0 = (i & 1) * kScanTpt * kScanThreads + tid;
+        if (left == kScanTpt) {
 #pragma unroll
-            for (int j = 0; j < kTpt; ++j)
-                if (t + j < len) {
-                    async_piece<sizeof(XP)>(&xs[(st * kTpt + j) * kScanThreads + tid], x + at + (size_t)j * D);
-                    async_piece<sizeof(GP)>(&gs[(st * kTpt + j) * kScanThreads + tid], g + at + (size_t)j * D);
+            for (int j = 0; j < kScanTpt; ++j) {
+                async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], g + from + (size_t)j * D);
+                async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], x + from + (size_t)j * D);
+            }
+        } else if (i < steps) {
+            const float id = identity_gate<kGate>(), z[4] = {id, id, id, id}, zero[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < kScanTpt; ++j) {
+                if (j < left) {
+                    async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], g + from + (size_t)j * D);
+                    async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], x + from + (size_t)j * D);
+                } else {
+                    gs[s0 + j * kScanThreads] = pack4<GT>(z);
+                    xs[s0 + j * kScanThreads] = pack4<XT>(zero);
                 }
+            }
         }
         async_commit();
     };
 
-    prefetch(0);
-    for (long long i = 0; i < steps; ++i) {
-        prefetch(i + 1);
+    prefetch(0, at);
+    for (int i = 0; i < steps; ++i, at += stride) {
+        prefetch(i + 1, at + stride);
         async_wait<1>();
-        const int st = (int)(i & 1);
-        const long long t = first_token(i);
-        float a[kTpt][kScanVec], b[kTpt][kScanVec];
+        const int p = i & 1, left = tokens_left(i);
+        const int s0 = p * kScanTpt * kScanThreads + tid;
+        float a[kScanTpt][kScanVec], b[kScanTpt][kScanVec];
         float A[kScanVec], H[kScanVec] = {0.f, 0.f, 0.f, 0.f};
-        Decay decay[kScanVec];
+        Decay<kGate> decay[kScanVec];
 #pragma unroll
-        for (int j = 0; j < kTpt; ++j) {
-            const bool valid = has_ch && t + j < len;
+        for (int j = 0; j < kScanTpt; ++j) {
             float xv[kScanVec], zv[kScanVec];
-            unpack4(xs[(st * kTpt + j) * kScanThreads + tid], xv);
-            unpack4(gs[(st * kTpt + j) * kScanThreads + tid], zv);
+            unpack4(xs[s0 + j * kScanThreads], xv);
+            unpack4(gs[s0 + j * kScanThreads], zv);
 #pragma unroll
             for (int c = 0; c < kScanVec; ++c) {
                 const Gated q = gate_value<kGate, kWrite, false>(zv[c], lower);
-                a[j][c] = valid ? q.a : 1.f;  // past the end: the identity map
-                b[j][c] = valid ? q.w * xv[c] : 0.f;
-                H[c] = fmaf(a[j][c], H[c], b[j][c]);
-                decay[c].then(a[j][c], valid ? q.c : 0.f);
+                a[j][c] = q.a;
+                b[j][c] = q.w * xv[c];
+                H[c] = fmaf(q.a, H[c], b[j][c]);
+                decay[c].then(q);
             }
         }
-#pragma unroll
-        for (int c = 0; c < kScanVec; ++c) A[c] = decay[c].value();
         // Inclusive composition over the warp's four pieces, then each piece's
         // predecessors alone (PA, PH).
         float PA[kScanVec], PH[kScanVec];
 #pragma unroll
         for (int c = 0; c < kScanVec; ++c) {
+            A[c] = decay[c].value();
 #pragma unroll
-            for (int off = kLanes; off < 32; off <<= 1) {
+            for (int off = kScanLanes; off < 32; off <<= 1) {
                 const float A2 = __shfl_up_sync(0xffffffffu, A[c], off);
                 const float H2 = __shfl_up_sync(0xffffffffu, H[c], off);
                 if (lane >= off) {
@@ -129,83 +133,65 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
                     A[c] *= A2;
                 }
             }
-            PA[c] = __shfl_up_sync(0xffffffffu, A[c], kLanes);
-            PH[c] = __shfl_up_sync(0xffffffffu, H[c], kLanes);
-            if (lane < kLanes) {
+            PA[c] = __shfl_up_sync(0xffffffffu, A[c], kScanLanes);
+            PH[c] = __shfl_up_sync(0xffffffffu, H[c], kScanLanes);
+            if (lane < kScanLanes) {
                 PA[c] = 1.f;
                 PH[c] = 0.f;
             }
         }
-        const int p = (int)(i & 1);
-        if (lane >= 32 - kLanes) {
+        // The maps' buffers alternate between steps: one is written again only
+        // after a barrier that every reader of it has arrived at.
+        if (lane >= 32 - kScanLanes) {
             *reinterpret_cast<float4 *>(&warp_map[p][warp][0][col]) = pack4<float>(A);
             *reinterpret_cast<float4 *>(&warp_map[p][warp][1][col]) = pack4<float>(H);
         }
         __syncthreads();
-        // This warp's predecessors in the CTA (WA, WH), and the CTA's own map.
-        float WA[kScanVec], WH[kScanVec], TA[kScanVec], TH[kScanVec];
-#pragma unroll
-        for (int c = 0; c < kScanVec; ++c) {
-            WA[c] = TA[c] = 1.f;
-            WH[c] = TH[c] = 0.f;
-        }
-#pragma unroll
-        for (int v = 0; v < kScanWarps; ++v) {
-            float A2[kScanVec], H2[kScanVec];
-            unpack4(*reinterpret_cast<const float4 *>(&warp_map[p][v][0][col]), A2);
-            unpack4(*reinterpret_cast<const float4 *>(&warp_map[p][v][1][col]), H2);
-#pragma unroll
-            for (int c = 0; c < kScanVec; ++c) {
-                if (v == warp) {
-                    WA[c] = TA[c];
-                    WH[c] = TH[c];
-                }
-                TH[c] = fmaf(A2[c], TH[c], H2[c]);
-                TA[c] *= A2[c];
-            }
-        }
         float h[kScanVec];
-        if (ranks == 1) {
+        auto apply = [&](float *state, const float (*map)[kScanCh]) {
+            float A2[kScanVec], H2[kScanVec];
+            unpack4(*reinterpret_cast<const float4 *>(&map[0][col]), A2);
+            unpack4(*reinterpret_cast<const float4 *>(&map[1][col]), H2);
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) {
-                h[c] = carry[c];
-                carry[c] = fmaf(TA[c], carry[c], TH[c]);
-            }
-        } else {
-            // Every CTA sends its map to every CTA of the cluster. The two
-            // buffers alternate: a CTA writes into one again only after a
-            // barrier that all arrive at having read it.
-            if (warp == 0)
-                for (int r = lane / kLanes; r < ranks; r += 32 / kLanes) {
-                    store_peer4((uint32_t)__cvta_generic_to_shared(&cta_map[p][rank][0][col]), r, TA);
-                    store_peer4((uint32_t)__cvta_generic_to_shared(&cta_map[p][rank][1][col]), r, TH);
+            for (int c = 0; c < kScanVec; ++c) state[c] = fmaf(A2[c], state[c], H2[c]);
+        };
+        if (ranks > 1) {
+            if (warp == 0) {  // one lane per channel: the CTA's map, sent to every CTA of the cluster
+                float TA = 1.f, TH = 0.f;
+#pragma unroll
+                for (int v = 0; v < kScanWarps; ++v) {
+                    const float A2 = warp_map[p][v][0][lane];
+                    TH = fmaf(A2, TH, warp_map[p][v][1][lane]);
+                    TA *= A2;
                 }
+                for (int r = 0; r < ranks; ++r) {
+                    store_peer(&cta_map[p][rank][0][lane], r, TA);
+                    store_peer(&cta_map[p][rank][1][lane], r, TH);
+                }
+            }
             cluster_sync();
-            for (int r = 0; r < ranks; ++r) {
-                float A2[kScanVec], H2[kScanVec];
-                unpack4(*reinterpret_cast<const float4 *>(&cta_map[p][r][0][col]), A2);
-                unpack4(*reinterpret_cast<const float4 *>(&cta_map[p][r][1][col]), H2);
+            for (int r = 0; r < rank; ++r) apply(carry, cta_map[p][r]);
 #pragma unroll
-                for (int c = 0; c < kScanVec; ++c) {
-                    if (r == rank) h[c] = carry[c];
-                    carry[c] = fmaf(A2[c], carry[c], H2[c]);
-                }
-            }
+            for (int c = 0; c < kScanVec; ++c) h[c] = carry[c];
+            for (int r = rank; r < ranks; ++r) apply(carry, cta_map[p][r]);
+            for (int v = 0; v < warp; ++v) apply(h, warp_map[p][v]);
+        } else {
+            for (int v = 0; v < warp; ++v) apply(carry, warp_map[p][v]);
+#pragma unroll
+            for (int c = 0; c < kScanVec; ++c) h[c] = carry[c];
+            for (int v = warp; v < kScanWarps; ++v) apply(carry, warp_map[p][v]);
         }
 #pragma unroll
-        for (int c = 0; c < kScanVec; ++c) {
-            h[c] = fmaf(WA[c], h[c], WH[c]);
-            h[c] = fmaf(PA[c], h[c], PH[c]);
-        }
-        if (carries && has_ch && t < len && t % KDA_SCAN_CARRY_TOKENS == 0)
-            *reinterpret_cast<float4 *>(carries + (size_t)carry_row(begin, n, t / KDA_SCAN_CARRY_TOKENS) * D + ch) =
+        for (int c = 0; c < kScanVec; ++c) h[c] = fmaf(PA[c], h[c], PH[c]);
+        if (carries && group == 0 && left > 0)
+            *reinterpret_cast<float4 *>(carries + (size_t)carry_row(begin, n, (long long)i * ranks + rank) * D + ch) =
                 pack4<float>(h);
-        XT *o = out + (size_t)(begin + t) * D + ch;
+        XT *o = out + at;
 #pragma unroll
-        for (int j = 0; j < kTpt; ++j) {
+        for (int j = 0; j < kScanTpt; ++j) {
 #pragma unroll
             for (int c = 0; c < kScanVec; ++c) h[c] = fmaf(a[j][c], h[c], b[j][c]);
-            if (has_ch && t + j < len) *reinterpret_cast<XP *>(o + (size_t)j * D) = pack4<XT>(h);
+            if (j < left) *reinterpret_cast<XP *>(o + (size_t)j * D) = pack4<XT>(h);
         }
     }
     async_wait<0>();
@@ -219,9 +205,9 @@ cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
     auto kernel = scan_fwd<XT, GT, kGate, kWrite>;
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
     if (err != cudaSuccess) return err;
-    const int blocks = (s.D + kBlockCh - 1) / kBlockCh;
+    const int blocks = (s.D + kScanCh - 1) / kScanCh;
     const long long units = (long long)s.num_seqs * blocks;
-    const int ranks = scan_ranks(units, s.cu ? s.tokens : s.T_fixed, S::kTile);
+    const int ranks = scan_ranks(units, s.cu ? s.tokens : s.T_fixed, 152 * S::per_sm);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ranks;

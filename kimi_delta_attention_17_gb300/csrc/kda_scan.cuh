@@ -2,6 +2,7 @@
 // the gate functions, four-channel pieces, and the composition of affine maps.
 #pragma once
 
+#include <stdlib.h>
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -27,11 +28,21 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 constexpr float kLog2E = 1.44269504088896341f;
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN stays NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 // a = e^x and c = 1 - a for a log-decay x <= 0. Near 0 both come from the
 // Taylor series of e^x - 1 (to x^7 / 7!, off by less than |x|^7 / 8! < 2e-8
 // relative for |x| < 0.35): 1 - e^x from a rounded e^x would lose the digits
-// of a small 1 - a, and a biased rounding of an a near 1 adds up over the
-// 1 / (1 - a) tokens that a slow channel remembers.
+// of a small 1 - a.
 __device__ __forceinline__ void decay_pair(float x, float &a, float &c) {
     float p = 1.f / 5040.f;
     p = fmaf(p, x, 1.f / 720.f);
@@ -47,56 +58,42 @@ __device__ __forceinline__ void decay_pair(float x, float &a, float &c) {
     c = small ? -m : 1.f - e;
 }
 
-// sigmoid(z) and 1 - sigmoid(z), each to a few units in its own last place
-// (the smaller of the two is t / (1 + t) with t = e^-|z| <= 1; the larger its
-// difference from 1).
+// sigmoid(z) and 1 - sigmoid(z) = t sigmoid(z) with t = e^-z, both accurate to
+// a few units in their own last place. Below -80 sigmoid(z) is taken as
+// e^-80 = 2e-35, so that t stays finite.
 __device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
-    const float t = ex2_approx(-fabsf(z) * kLog2E);
-    const float m = t * rcp_approx(1.f + t);
-    const float l = 1.f - m;
-    s = z >= 0.f ? l : m;
-    c = z >= 0.f ? m : l;
+    const float t = ex2_approx(max_nan(z, -80.f) * -kLog2E);
+    s = rcp_approx(1.f + t);
+    c = t * s;
 }
 
-// What one gate value gives: a, c = 1 - a, the input weight w, and, for the
-// backward pass, slope = dlog a/dg and wslope = dw/dg.
+// What one gate value gives: a, the input weight w, 1 - a or log a (`rest`,
+// for Decay), and, for the backward pass, slope = dlog a/dg and wslope = dw/dg.
 struct Gated {
-    float a, c, w, slope, wslope;
-};
-
-// The decay over a thread's tokens: a product A of decays, and with it C = 1 - A
-// from the tokens' 1 - a. Slow channels need C: of two factors 1 - p and 1 - q
-// with p q < 2^-25 the rounded product loses p q every time, always to the same
-// side, which over the thousands of tokens that such a channel remembers comes
-// to hundreds of roundings (measured at a ~ 0.9999 over 6000 tokens: 430 x 2^-24
-// off by products alone).
-struct Decay {
-    float A = 1.f, C = 0.f;
-    __device__ __forceinline__ void then(float a, float c) {
-        A *= a;
-        C = fmaf(-C, c, C + c);
-    }
-    __device__ __forceinline__ float value() const { return C < 0.5f ? 1.f - C : A; }
+    float a, w, rest, slope, wslope;
 };
 
 template <int kGate, int kWrite, bool kGrad>
 __device__ __forceinline__ Gated gate_value(float z, float lower) {
     Gated r;
-    float c;
+    float c;  // 1 - a
     r.slope = 1.f;
     if (kGate == KDA_GATE_LOGSIGMOID) {
         sigmoid_pair(z, r.a, c);
-        r.slope = c;
-    } else if (kGate == KDA_GATE_BOUNDED) {
-        float s, sc;
-        sigmoid_pair(z, s, sc);
-        const float la = lower * s;
-        decay_pair(la, r.a, c);
-        r.slope = la * sc;
+        r.slope = r.rest = c;
     } else {
-        decay_pair(z, r.a, c);
+        r.rest = z;
+        if (kGate == KDA_GATE_BOUNDED) {
+            float s, sc;
+            sigmoid_pair(z, s, sc);
+            r.rest = lower * s;
+            r.slope = r.rest * sc;
+        }
+        if (kWrite == KDA_WRITE_PLAIN)
+            r.a = ex2_approx(r.rest * kLog2E);
+        else
+            decay_pair(r.rest, r.a, c);
     }
-    r.c = c;
     r.wslope = 0.f;
     if (kWrite == KDA_WRITE_PLAIN) {
         r.w = 1.f;
@@ -104,7 +101,7 @@ __device__ __forceinline__ Gated gate_value(float z, float lower) {
         r.w = c;
         if (kGrad) r.wslope = -r.a * r.slope;  // dw/dlog a = -a
     } else {
-        r.w = sqrtf(c * (1.f + r.a));  // 1 - a^2 from its factors
+        r.w = sqrt_approx(fmaf(c, r.a, c));  // 1 - a^2 from its factors
         // dw/dlog a = -a^2 / w. Under the logistic gate dlog a/dg = 1 - a
         // cancels the division: w^2 = (1 - a)(1 + a).
         if (kGrad)
@@ -114,6 +111,40 @@ __device__ __forceinline__ Gated gate_value(float z, float lower) {
     }
     return r;
 }
+
+// The gate value of the identity map (a = 1), which stands past a sequence's end.
+template <int kGate>
+__device__ __forceinline__ float identity_gate() {
+    return kGate == KDA_GATE_LOG ? 0.f
+                                 : __uint_as_float(kGate == KDA_GATE_LOGSIGMOID ? 0x7f800000u : 0xff800000u);
+}
+
+// The decay A over a thread's tokens. Products of rounded decays will not do
+// for slow channels: of two factors 1 - p and 1 - q with p q < 2^-25 the
+// rounded product loses p q every time, always to the same side, which over
+// the thousands of tokens that such a channel remembers comes to hundreds of
+// roundings (measured at a ~ 0.9999 over 6000 tokens: 430 x 2^-24). A
+// log-decay is summed instead; under the logistic gate, which gives 1 - a,
+// 1 - A is carried beside the product and used while A > 1/2.
+template <int kGate>
+struct Decay {
+    float sum = 0.f;
+    __device__ __forceinline__ void then(const Gated &q) { sum += q.rest; }
+    __device__ __forceinline__ float value() const {
+        float a, c;
+        decay_pair(sum, a, c);
+        return a;
+    }
+};
+template <>
+struct Decay<KDA_GATE_LOGSIGMOID> {
+    float A = 1.f, C = 0.f;
+    __device__ __forceinline__ void then(const Gated &q) {
+        A *= q.a;
+        C = fmaf(-C, q.rest, C + q.rest);
+    }
+    __device__ __forceinline__ float value() const { return C < 0.5f ? 1.f - C : A; }
+};
 
 // Four values as they lie in memory.
 template <typename T> struct Piece;
@@ -137,6 +168,18 @@ template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(const float *x
     const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
+
+// The tiling that the forward and the backward scan share.
+constexpr int kScanLanes = 8;                         // threads across the channels
+constexpr int kScanCh = kScanLanes * kScanVec;        // channels per CTA
+constexpr int kScanThreads = 128;
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kScanTpt = 8;                           // tokens per thread
+constexpr int kScanTile = kScanThreads / kScanLanes * kScanTpt;
+constexpr int kScanStages = 2;
+constexpr int kScanMaxRanks = 8;
+static_assert(kScanTile == KDA_SCAN_CARRY_TOKENS, "a tile begins at a saved state");
+static_assert(kScanCh == 32, "a warp composes the CTA's maps with one lane per channel");
 
 // Copies one piece to shared memory without passing through registers.
 template <int kBytes>
@@ -163,12 +206,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_peer4(uint32_t addr, uint32_t rank, const float *v) {
+__device__ __forceinline__ void store_peer(float *mine, uint32_t rank, float v) {
     uint32_t peer;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer), "f"(v[0]), "f"(v[1]),
-                 "f"(v[2]), "f"(v[3])
-                 : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(peer)
+                 : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer), "f"(v) : "memory");
 }
 
 // Tokens [begin, end) of sequence n among `tokens`: offsets are clamped, so
@@ -218,11 +261,12 @@ struct ScanStepArgs {
 cudaError_t launch_scan_step(const ScanStepArgs &s, cudaStream_t stream);
 
 // CTAs per cluster, i.e. tiles of one (sequence, channel block) in flight at
-// once: more while the units alone leave SMs without work, up to the tiles
-// that the longest sequence can have.
-inline int scan_ranks(long long units, long long longest, int tile) {
+// once: as many as still run all at the same time (`slots` CTAs fit the GPU),
+// up to the tiles that the longest sequence can have.
+inline int scan_ranks(long long units, long long longest, long long slots) {
+    if (const char *e = getenv("KDA_RANKS")) return atoi(e);
     int ranks = 1;
-    while (ranks < 8 && units * ranks < 2 * 152 && (long long)ranks * tile < longest) ranks *= 2;
+    while (ranks < kScanMaxRanks && 2 * ranks * units <= slots && (long long)ranks * kScanTile < longest) ranks *= 2;
     return ranks;
 }
 
