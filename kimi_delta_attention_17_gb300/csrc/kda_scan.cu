@@ -22,13 +22,23 @@
 namespace kda {
 namespace {
 
+#ifndef FWD_STAGES
+#define FWD_STAGES 2
+#endif
+struct FwdShared {
+    float map[kScanGroups][2][kScanCh];       // (A, H) of each piece; then H gives way to the state entering it
+    float2 warp_map[2][kScanWarps][kScanCh];  // (A, H) of each warp's tokens
+    ClusterMaps peers;
+};
 template <typename XT, typename GT>
 struct FwdShape {
     using XP = typename Piece<XT>::type;
     using GP = typename Piece<GT>::type;
-    static constexpr size_t slots = (size_t)kScanStages * kScanTpt * kScanThreads;
+    static constexpr int stages = FWD_STAGES;
+    static constexpr size_t slots = (size_t)stages * kScanTpt * kScanThreads;
     static constexpr size_t smem = slots * (sizeof(XP) + sizeof(GP));
-    static constexpr int per_sm = smem <= 50 * 1024 ? 4 : 3;  // CTAs
+    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(FwdShared) + kCtaReserved));
+    static constexpr int per_sm = kScanTpt == 4 ? (fit < 3 ? fit : 3) : (fit < 4 ? fit : 4);  // CTAs
 };
 
 template <typename XT, typename GT, int kGate, int kWrite>
@@ -43,17 +53,21 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     extern __shared__ __align__(16) unsigned char smem_raw[];
     GP *gs = reinterpret_cast<GP *>(smem_raw);
     XP *xs = reinterpret_cast<XP *>(smem_raw + S::slots * sizeof(GP));
-    __shared__ __align__(16) float warp_map[2][kScanWarps][2][kScanCh];    // (A, H) of each warp
-    __shared__ __align__(16) float cta_map[2][kScanMaxRanks][2][kScanCh];  // and of each CTA
+    __shared__ __align__(16) FwdShared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
     const int n = (int)(unit / (unsigned)blocks);
+    const int ch0 = (int)(unit % (unsigned)blocks) * kScanCh;
     const int col = kScanVec * (lane & (kScanLanes - 1));
-    const int ch = (int)(unit % (unsigned)blocks) * kScanCh + col;
+    const int ch = ch0 + col;
     const bool has_ch = ch < D;
     const int group = tid / kScanLanes;
+    // In every warp, lane = channel: the state at the cluster's next tiles. Read
+    // before the cluster's first barrier: final_state may be the same memory.
+    float carry = init && ch0 + lane < D ? init[(size_t)n * D + ch0 + lane] : 0.f;
+    if (ranks > 1) cluster_maps_init(sh.peers);
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
@@ -61,31 +75,28 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     const int super = kScanTile * ranks;  // tokens per cluster step
     const int steps = (int)(((long long)len + super - 1) / super);
 
-    float carry[kScanVec] = {0.f, 0.f, 0.f, 0.f};
-    if (init && has_ch) unpack4(*reinterpret_cast<const float4 *>(init + (size_t)n * D + ch), carry);
-
-    // Tokens of this thread in step i that lie before the sequence's end.
-    auto tokens_left = [&](int i) {
-        const long long t = ((long long)i * ranks + rank) * kScanTile + group * kScanTpt;
-        return has_ch ? (int)min(max(len - t, 0LL), (long long)kScanTpt) : 0;
-    };
-    size_t at = (size_t)(begin + (long long)rank * kScanTile + group * kScanTpt) * D + ch;  // first element of a step
+    // Of this step: tokens from this thread's first one to the sequence's end
+    // (none left where negative), and the first one's element.
+    int left = has_ch ? len - (rank * kScanTile + group * kScanTpt) : -1;
+    const int less = has_ch ? super : 0;
+    size_t at = (size_t)(begin + (long long)rank * kScanTile + group * kScanTpt) * D + ch;
     const size_t stride = (size_t)super * D;
-    auto prefetch = [&](int i, size_t from) {
-        const int left = i < steps ? tokens_left(i) : 0;
-        const int s0 = (i & 1) * kScanTpt * kScanThreads + tid;
-        if (left == kScanTpt) {
+    auto prefetch = [&](int i, int left, size_t from) {
+        const int s0 = i % S::stages * kScanTpt * kScanThreads + tid;
+        const GT *gp = g + from;
+        const XT *xp = x + from;
+        if (left >= kScanTpt) {
 #pragma unroll
             for (int j = 0; j < kScanTpt; ++j) {
-                async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], g + from + (size_t)j * D);
-                async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], x + from + (size_t)j * D);
+                async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], gp + (size_t)j * D);
+                async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], xp + (size_t)j * D);
             }
         } else if (i < steps) {
-            const float id = identity_gate<kGate>(), z[4] = {id, id, id, id}, zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const F2 id = f2(identity_gate<kGate>()), z[2] = {id, id}, zero[2] = {{0}, {0}};
             for (int j = 0; j < kScanTpt; ++j) {
                 if (j < left) {
-                    async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], g + from + (size_t)j * D);
-                    async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], x + from + (size_t)j * D);
+                    async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], gp + (size_t)j * D);
+                    async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], xp + (size_t)j * D);
                 } else {
                     gs[s0 + j * kScanThreads] = pack4<GT>(z);
                     xs[s0 + j * kScanThreads] = pack4<XT>(zero);
@@ -95,108 +106,105 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
         async_commit();
     };
 
-    prefetch(0, at);
-    for (int i = 0; i < steps; ++i, at += stride) {
-        prefetch(i + 1, at + stride);
-        async_wait<1>();
-        const int p = i & 1, left = tokens_left(i);
-        const int s0 = p * kScanTpt * kScanThreads + tid;
-        float a[kScanTpt][kScanVec], b[kScanTpt][kScanVec];
-        float A[kScanVec], H[kScanVec] = {0.f, 0.f, 0.f, 0.f};
-        Decay<kGate> decay[kScanVec];
 #pragma unroll
-        for (int j = 0; j < kScanTpt; ++j) {
-            float xv[kScanVec], zv[kScanVec];
-            unpack4(xs[s0 + j * kScanThreads], xv);
-            unpack4(gs[s0 + j * kScanThreads], zv);
+    for (int i = 0; i < S::stages; ++i) prefetch(i, left - i * less, at + i * stride);
+    for (int i = 0; i < steps; ++i, at += stride, left -= less) {
+        async_wait<S::stages - 1>();
+        const int s0 = i % S::stages * kScanTpt * kScanThreads + tid;
+        F2 a[kScanTpt][kScanPairs], b[kScanTpt][kScanPairs];
+        {
+            F2 A[kScanPairs], H[kScanPairs] = {{0}, {0}};
+            Decay<kGate> decay[kScanPairs];
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) {
-                const Gated q = gate_value<kGate, kWrite, false>(zv[c], lower);
-                a[j][c] = q.a;
-                b[j][c] = q.w * xv[c];
-                H[c] = fmaf(q.a, H[c], b[j][c]);
-                decay[c].then(q);
-            }
-        }
-        // Inclusive composition over the warp's four pieces, then each piece's
-        // predecessors alone (PA, PH).
-        float PA[kScanVec], PH[kScanVec];
+            for (int j = 0; j < kScanTpt; ++j) {
+                F2 xv[kScanPairs], zv[kScanPairs];
+                unpack4(xs[s0 + j * kScanThreads], xv);
+                unpack4(gs[s0 + j * kScanThreads], zv);
 #pragma unroll
-        for (int c = 0; c < kScanVec; ++c) {
-            A[c] = decay[c].value();
-#pragma unroll
-            for (int off = kScanLanes; off < 32; off <<= 1) {
-                const float A2 = __shfl_up_sync(0xffffffffu, A[c], off);
-                const float H2 = __shfl_up_sync(0xffffffffu, H[c], off);
-                if (lane >= off) {
-                    H[c] = fmaf(A[c], H2, H[c]);
-                    A[c] *= A2;
+                for (int c = 0; c < kScanPairs; ++c) {
+                    const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
+                    a[j][c] = q.a;
+                    b[j][c] = written<kWrite>(q.a, q.c, xv[c]);
+                    H[c] = fma2(q.a, H[c], b[j][c]);
+                    decay[c].then(q);
                 }
             }
-            PA[c] = __shfl_up_sync(0xffffffffu, A[c], kScanLanes);
-            PH[c] = __shfl_up_sync(0xffffffffu, H[c], kScanLanes);
-            if (lane < kScanLanes) {
-                PA[c] = 1.f;
-                PH[c] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kScanPairs; ++c) A[c] = decay[c].value();
+            *reinterpret_cast<float4 *>(&sh.map[group][0][col]) = pack4<float>(A);
+            *reinterpret_cast<float4 *>(&sh.map[group][1][col]) = pack4<float>(H);
+        }
+        prefetch(i + S::stages, left - S::stages * less, at + S::stages * stride);  // into the slots just read
+        // Lane = channel: the warp's pieces are composed in order.
+        __syncwarp();
+        float A[kWarpGroups], H[kWarpGroups];
+        {
+            float PA = 1.f, PH = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWarpGroups; ++v) {
+                A[v] = sh.map[warp * kWarpGroups + v][0][lane];
+                H[v] = sh.map[warp * kWarpGroups + v][1][lane];
             }
-        }
-        // The maps' buffers alternate between steps: one is written again only
-        // after a barrier that every reader of it has arrived at.
-        if (lane >= 32 - kScanLanes) {
-            *reinterpret_cast<float4 *>(&warp_map[p][warp][0][col]) = pack4<float>(A);
-            *reinterpret_cast<float4 *>(&warp_map[p][warp][1][col]) = pack4<float>(H);
-        }
-        __syncthreads();
-        float h[kScanVec];
-        auto apply = [&](float *state, const float (*map)[kScanCh]) {
-            float A2[kScanVec], H2[kScanVec];
-            unpack4(*reinterpret_cast<const float4 *>(&map[0][col]), A2);
-            unpack4(*reinterpret_cast<const float4 *>(&map[1][col]), H2);
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) state[c] = fmaf(A2[c], state[c], H2[c]);
-        };
-        if (ranks > 1) {
-            if (warp == 0) {  // one lane per channel: the CTA's map, sent to every CTA of the cluster
-                float TA = 1.f, TH = 0.f;
+            for (int v = 0; v < kWarpGroups; ++v) {
+                PH = fmaf(A[v], PH, H[v]);
+                PA *= A[v];
+            }
+            sh.warp_map[i & 1][warp][lane] = make_float2(PA, PH);
+        }
+        __syncthreads();  // warp_map's halves alternate: the only barrier of a step
+        {
+            float2 m[kScanWarps];
 #pragma unroll
-                for (int v = 0; v < kScanWarps; ++v) {
-                    const float A2 = warp_map[p][v][0][lane];
-                    TH = fmaf(A2, TH, warp_map[p][v][1][lane]);
-                    TA *= A2;
+            for (int v = 0; v < kScanWarps; ++v) m[v] = sh.warp_map[i & 1][v][lane];
+            float first = carry;  // the state entering the CTA's tile
+            if (ranks > 1) {
+                if (warp == 0) {
+                    float TA = 1.f, TH = 0.f;
+#pragma unroll
+                    for (int v = 0; v < kScanWarps; ++v) {
+                        TH = fmaf(m[v].x, TH, m[v].y);
+                        TA *= m[v].x;
+                    }
+                    cluster_maps_send(sh.peers, i, rank, ranks, TA, TH);
                 }
+                if (!cluster_maps_wait(sh.peers, i)) carry = __uint_as_float(0x7fc00000u);
                 for (int r = 0; r < ranks; ++r) {
-                    store_peer(&cta_map[p][rank][0][lane], r, TA);
-                    store_peer(&cta_map[p][rank][1][lane], r, TH);
+                    if (r == rank) first = carry;
+                    const float2 t = sh.peers.map[i & 1][r][lane];
+                    carry = fmaf(t.x, carry, t.y);
                 }
             }
-            cluster_sync();
-            for (int r = 0; r < rank; ++r) apply(carry, cta_map[p][r]);
+            // The tile begins at a token whose entering state the backward pass needs.
+            const long long tile = (long long)i * ranks + rank;
+            if (carries && warp == 0 && tile * kScanTile < len && ch0 + lane < D)
+                carries[(size_t)carry_row(begin, n, tile) * D + ch0 + lane] = first;
+            float mine = 0.f;  // the state entering the warp's tokens
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) h[c] = carry[c];
-            for (int r = rank; r < ranks; ++r) apply(carry, cta_map[p][r]);
-            for (int v = 0; v < warp; ++v) apply(h, warp_map[p][v]);
-        } else {
-            for (int v = 0; v < warp; ++v) apply(carry, warp_map[p][v]);
+            for (int v = 0; v < kScanWarps; ++v) {
+                if (v == warp) mine = first;
+                first = fmaf(m[v].x, first, m[v].y);
+            }
+            if (ranks == 1) carry = first;
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) h[c] = carry[c];
-            for (int v = warp; v < kScanWarps; ++v) apply(carry, warp_map[p][v]);
+            for (int v = 0; v < kWarpGroups; ++v) {
+                sh.map[warp * kWarpGroups + v][1][lane] = mine;
+                mine = fmaf(A[v], mine, H[v]);
+            }
         }
-#pragma unroll
-        for (int c = 0; c < kScanVec; ++c) h[c] = fmaf(PA[c], h[c], PH[c]);
-        if (carries && group == 0 && left > 0)
-            *reinterpret_cast<float4 *>(carries + (size_t)carry_row(begin, n, (long long)i * ranks + rank) * D + ch) =
-                pack4<float>(h);
+        __syncwarp();
+        F2 h[kScanPairs];
+        unpack4(*reinterpret_cast<const float4 *>(&sh.map[group][1][col]), h);
         XT *o = out + at;
 #pragma unroll
         for (int j = 0; j < kScanTpt; ++j) {
 #pragma unroll
-            for (int c = 0; c < kScanVec; ++c) h[c] = fmaf(a[j][c], h[c], b[j][c]);
+            for (int c = 0; c < kScanPairs; ++c) h[c] = fma2(a[j][c], h[c], b[j][c]);
             if (j < left) *reinterpret_cast<XP *>(o + (size_t)j * D) = pack4<XT>(h);
         }
     }
     async_wait<0>();
-    if (final_state && has_ch && rank == 0 && group == 0)
-        *reinterpret_cast<float4 *>(final_state + (size_t)n * D + ch) = pack4<float>(carry);
+    if (final_state && warp == 0 && rank == 0 && ch0 + lane < D) final_state[(size_t)n * D + ch0 + lane] = carry;
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
@@ -236,17 +244,17 @@ scan_step(const XT *__restrict__ x, const GT *__restrict__ g, float *__restrict_
     const int n = (int)(i / per_row), c4 = (int)(i % per_row);
     const long long slot = slots ? slots[n] : n;
     const size_t at = (size_t)i * kScanVec;
-    float h[kScanVec] = {0.f, 0.f, 0.f, 0.f};
+    F2 h[kScanPairs] = {{0}, {0}};
     if (slot >= 0 && slot < num_slots) {
-        float xv[kScanVec], zv[kScanVec];
+        F2 xv[kScanPairs], zv[kScanPairs];
         float4 *sp = reinterpret_cast<float4 *>(state) + (size_t)slot * per_row + c4;
         unpack4(*sp, h);
         unpack4(*reinterpret_cast<const typename Piece<XT>::type *>(x + at), xv);
         unpack4(*reinterpret_cast<const typename Piece<GT>::type *>(g + at), zv);
 #pragma unroll
-        for (int c = 0; c < kScanVec; ++c) {
-            const Gated q = gate_value<kGate, kWrite, false>(zv[c], lower);
-            h[c] = fmaf(q.a, h[c], q.w * xv[c]);
+        for (int c = 0; c < kScanPairs; ++c) {
+            const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
+            h[c] = fma2(q.a, h[c], written<kWrite>(q.a, q.c, xv[c]));
         }
         *sp = pack4<float>(h);
     }

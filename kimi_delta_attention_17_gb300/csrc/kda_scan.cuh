@@ -33,83 +33,120 @@ __device__ __forceinline__ float sqrt_approx(float x) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rsqrt_approx(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float max_nan(float x, float y) {  // NaN stays NaN
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
+// Two fp32 values that one instruction takes together (FFMA2 and its kin): the
+// scans are short of issue slots before they are short of anything else.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+template <typename F>
+__device__ __forceinline__ F2 each(F2 x, F f) {
+    float lo, hi;
+    split(x, lo, hi);
+    return f2(f(lo), f(hi));
+}
+
 // a = e^x and c = 1 - a for a log-decay x <= 0. Near 0 both come from the
 // Taylor series of e^x - 1 (to x^7 / 7!, off by less than |x|^7 / 8! < 2e-8
 // relative for |x| < 0.35): 1 - e^x from a rounded e^x would lose the digits
 // of a small 1 - a.
-__device__ __forceinline__ void decay_pair(float x, float &a, float &c) {
-    float p = 1.f / 5040.f;
-    p = fmaf(p, x, 1.f / 720.f);
-    p = fmaf(p, x, 1.f / 120.f);
-    p = fmaf(p, x, 1.f / 24.f);
-    p = fmaf(p, x, 1.f / 6.f);
-    p = fmaf(p, x, 0.5f);
-    p = fmaf(p, x, 1.f);
-    const float m = p * x;  // e^x - 1
-    const float e = ex2_approx(x * kLog2E);
-    const bool small = fabsf(x) < 0.35f;
-    a = small ? 1.f + m : e;
-    c = small ? -m : 1.f - e;
+__device__ __forceinline__ void decay_pair(F2 x, F2 &a, F2 &c) {
+    F2 p = fma2(f2(1.f / 5040.f), x, f2(1.f / 720.f));
+    p = fma2(p, x, f2(1.f / 120.f));
+    p = fma2(p, x, f2(1.f / 24.f));
+    p = fma2(p, x, f2(1.f / 6.f));
+    p = fma2(p, x, f2(0.5f));
+    p = fma2(p, x, f2(1.f));
+    const F2 m = mul2(p, x);  // e^x - 1
+    const F2 e = each(mul2(x, f2(kLog2E)), ex2_approx);
+    const F2 e1 = add2(e, f2(-1.f)), m1 = add2(m, f2(1.f));
+    float x0, x1, m0[2], e0[2], e10[2], m10[2];
+    split(x, x0, x1);
+    split(m, m0[0], m0[1]);
+    split(e, e0[0], e0[1]);
+    split(e1, e10[0], e10[1]);
+    split(m1, m10[0], m10[1]);
+    const bool s0 = fabsf(x0) < 0.35f, s1 = fabsf(x1) < 0.35f;
+    a = f2(s0 ? m10[0] : e0[0], s1 ? m10[1] : e0[1]);
+    c = f2(-(s0 ? m0[0] : e10[0]), -(s1 ? m0[1] : e10[1]));
 }
 
 // sigmoid(z) and 1 - sigmoid(z) = t sigmoid(z) with t = e^-z, both accurate to
 // a few units in their own last place. Below -80 sigmoid(z) is taken as
 // e^-80 = 2e-35, so that t stays finite.
-__device__ __forceinline__ void sigmoid_pair(float z, float &s, float &c) {
-    const float t = ex2_approx(max_nan(z, -80.f) * -kLog2E);
-    s = rcp_approx(1.f + t);
-    c = t * s;
+__device__ __forceinline__ void sigmoid_pair(F2 z, F2 &s, F2 &c) {
+    const F2 t = each(mul2(each(z, [](float v) { return max_nan(v, -80.f); }), f2(-kLog2E)), ex2_approx);
+    s = each(add2(t, f2(1.f)), rcp_approx);
+    c = mul2(t, s);
 }
 
-// What one gate value gives: a, the input weight w, 1 - a or log a (`rest`,
-// for Decay), and, for the backward pass, slope = dlog a/dg and wslope = dw/dg.
+// What two gate values give: a, c = 1 - a (formed where the write or the gate
+// has it), and log a or 1 - a (`rest`) for Decay.
 struct Gated {
-    float a, w, rest, slope, wslope;
+    F2 a, c, rest;
 };
-
-template <int kGate, int kWrite, bool kGrad>
-__device__ __forceinline__ Gated gate_value(float z, float lower) {
+template <int kGate, int kWrite>
+__device__ __forceinline__ Gated gate_value(F2 z, float lower) {
     Gated r;
-    float c;  // 1 - a
-    r.slope = 1.f;
     if (kGate == KDA_GATE_LOGSIGMOID) {
-        sigmoid_pair(z, r.a, c);
-        r.slope = r.rest = c;
-    } else {
-        r.rest = z;
-        if (kGate == KDA_GATE_BOUNDED) {
-            float s, sc;
-            sigmoid_pair(z, s, sc);
-            r.rest = lower * s;
-            r.slope = r.rest * sc;
-        }
-        if (kWrite == KDA_WRITE_PLAIN)
-            r.a = ex2_approx(r.rest * kLog2E);
-        else
-            decay_pair(r.rest, r.a, c);
+        sigmoid_pair(z, r.a, r.c);
+        r.rest = r.c;
+        return r;
     }
-    r.wslope = 0.f;
+    r.rest = z;
+    if (kGate == KDA_GATE_BOUNDED) {
+        F2 s, sc;
+        sigmoid_pair(z, s, sc);
+        r.rest = mul2(f2(lower), s);
+    }
     if (kWrite == KDA_WRITE_PLAIN) {
-        r.w = 1.f;
-    } else if (kWrite == KDA_WRITE_COMPLEMENT) {
-        r.w = c;
-        if (kGrad) r.wslope = -r.a * r.slope;  // dw/dlog a = -a
+        r.a = each(mul2(r.rest, f2(kLog2E)), ex2_approx);
+        r.c = f2(0.f);  // not used
     } else {
-        r.w = sqrt_approx(fmaf(c, r.a, c));  // 1 - a^2 from its factors
-        // dw/dlog a = -a^2 / w. Under the logistic gate dlog a/dg = 1 - a
-        // cancels the division: w^2 = (1 - a)(1 + a).
-        if (kGrad)
-            r.wslope = kGate == KDA_GATE_LOGSIGMOID
-                           ? -r.a * r.a * r.w * rcp_approx(1.f + r.a)
-                           : (r.w > 0.f ? -r.a * r.a * r.slope * rcp_approx(r.w) : 0.f);
+        decay_pair(r.rest, r.a, r.c);
     }
     return r;
+}
+// w x: the input as it enters the state; 1 - a^2 is taken from its factors.
+template <int kWrite>
+__device__ __forceinline__ F2 written(F2 a, F2 c, F2 x) {
+    if (kWrite == KDA_WRITE_PLAIN) return x;
+    if (kWrite == KDA_WRITE_COMPLEMENT) return mul2(c, x);
+    return mul2(each(fma2(c, a, c), sqrt_approx), x);
 }
 
 // The gate value of the identity map (a = 1), which stands past a sequence's end.
@@ -128,22 +165,27 @@ __device__ __forceinline__ float identity_gate() {
 // 1 - A is carried beside the product and used while A > 1/2.
 template <int kGate>
 struct Decay {
-    float sum = 0.f;
-    __device__ __forceinline__ void then(const Gated &q) { sum += q.rest; }
-    __device__ __forceinline__ float value() const {
-        float a, c;
+    F2 sum = {0};
+    __device__ __forceinline__ void then(const Gated &q) { sum = add2(sum, q.rest); }
+    __device__ __forceinline__ F2 value() const {
+        F2 a, c;
         decay_pair(sum, a, c);
         return a;
     }
 };
 template <>
 struct Decay<KDA_GATE_LOGSIGMOID> {
-    float A = 1.f, C = 0.f;
+    F2 A = f2(1.f), C = {0};
     __device__ __forceinline__ void then(const Gated &q) {
-        A *= q.a;
-        C = fmaf(-C, q.rest, C + q.rest);
+        C = fma2(q.rest, A, C);
+        A = mul2(A, q.a);
     }
-    __device__ __forceinline__ float value() const { return C < 0.5f ? 1.f - C : A; }
+    __device__ __forceinline__ F2 value() const {
+        float a0, a1, c0, c1;
+        split(A, a0, a1);
+        split(C, c0, c1);
+        return f2(c0 < 0.5f ? 1.f - c0 : a0, c1 < 0.5f ? 1.f - c1 : a1);
+    }
 };
 
 // Four values as they lie in memory.
@@ -151,35 +193,44 @@ template <typename T> struct Piece;
 template <> struct Piece<float> { using type = float4; };
 template <> struct Piece<__nv_bfloat16> { using type = uint2; };
 
-__device__ __forceinline__ void unpack4(const float4 &r, float *x) {
-    x[0] = r.x; x[1] = r.y; x[2] = r.z; x[3] = r.w;
+__device__ __forceinline__ void unpack4(const float4 &r, F2 *x) {
+    x[0] = f2(r.x, r.y);
+    x[1] = f2(r.z, r.w);
 }
-__device__ __forceinline__ void unpack4(const uint2 &r, float *x) {
-    x[0] = __uint_as_float(r.x << 16);
-    x[1] = __uint_as_float(r.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(r.y << 16);
-    x[3] = __uint_as_float(r.y & 0xFFFF0000u);
+__device__ __forceinline__ void unpack4(const uint2 &r, F2 *x) {
+    x[0] = f2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
+    x[1] = f2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
 }
-template <typename T> __device__ __forceinline__ typename Piece<T>::type pack4(const float *x);
-template <> __device__ __forceinline__ float4 pack4<float>(const float *x) {
-    return make_float4(x[0], x[1], x[2], x[3]);
+template <typename T> __device__ __forceinline__ typename Piece<T>::type pack4(const F2 *x);
+template <> __device__ __forceinline__ float4 pack4<float>(const F2 *x) {
+    float4 r;
+    split(x[0], r.x, r.y);
+    split(x[1], r.z, r.w);
+    return r;
 }
-template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(const float *x) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(const F2 *x) {
+    const float4 r = pack4<float>(x);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(r.x, r.y), hi = __floats2bfloat162_rn(r.z, r.w);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
 }
 
 // The tiling that the forward and the backward scan share.
+constexpr int kScanPairs = kScanVec / 2;
 constexpr int kScanLanes = 8;                         // threads across the channels
 constexpr int kScanCh = kScanLanes * kScanVec;        // channels per CTA
-constexpr int kScanThreads = 128;
+#ifndef SCAN_THREADS
+#define SCAN_THREADS 128
+#endif
+constexpr int kScanThreads = SCAN_THREADS;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanTpt = 8;                           // tokens per thread
-constexpr int kScanTile = kScanThreads / kScanLanes * kScanTpt;
-constexpr int kScanStages = 2;
+constexpr int kScanGroups = kScanThreads / kScanLanes;  // pieces of consecutive tokens per tile
+constexpr int kWarpGroups = 32 / kScanLanes;            // and per warp
+constexpr int kScanTpt = 128 / kScanGroups;                           // tokens per thread
+constexpr int kScanTile = kScanGroups * kScanTpt;
+constexpr size_t kSmSmem = 228 * 1024, kCtaReserved = 1024;  // shared memory of an SM, and what each CTA takes beside its own
 constexpr int kScanMaxRanks = 8;
 static_assert(kScanTile == KDA_SCAN_CARRY_TOKENS, "a tile begins at a saved state");
-static_assert(kScanCh == 32, "a warp composes the CTA's maps with one lane per channel");
+static_assert(kScanCh == 32, "one lane per channel composes a tile's maps");
 
 // Copies one piece to shared memory without passing through registers.
 template <int kBytes>
@@ -201,17 +252,64 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// A barrier over every thread of the cluster; what a thread wrote before it,
-// into any CTA's shared memory, is seen after it.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_peer(float *mine, uint32_t rank, float v) {
-    uint32_t peer;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(peer)
-                 : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer), "f"(v) : "memory");
+
+// The exchange of tile maps between the CTAs of a cluster. Each step every CTA
+// sends its map (two floats per channel) to every CTA, itself included, by
+// asynchronous stores that the receiver's mbarrier counts: no fence, which
+// would wait for the outputs on their way to memory. Buffers alternate between
+// steps: a CTA sends step i + 2 only after it has everyone's maps of step
+// i + 1, which each sends after a CTA barrier that follows its reads of step i.
+struct ClusterMaps {
+    float2 map[2][kScanMaxRanks][kScanCh];
+    unsigned long long bar[2];
+};
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// All threads of the cluster, once.
+__device__ __forceinline__ void cluster_maps_init(ClusterMaps &m) {
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&m.bar[b])) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    cluster_sync();
+}
+// One warp, lane = channel: sends (a, b) as step `step`'s map of this CTA.
+__device__ __forceinline__ void cluster_maps_send(ClusterMaps &m, int step, int rank, int ranks, float a, float b) {
+    const int lane = threadIdx.x & 31, p = step & 1;
+    const uint32_t bar = smem_addr(&m.bar[p]), mine = smem_addr(&m.map[p][rank][lane]);
+    if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                     "r"(ranks * kScanCh * (int)sizeof(float2))
+                     : "memory");
+    for (int r = 0; r < ranks; ++r) {
+        uint32_t to, to_bar;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(r));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                     "f"(a), "f"(b), "r"(to_bar)
+                     : "memory");
+    }
+}
+// Waits for the maps of step `step`. The wait always ends (the CTAs of a cluster
+// run together and send as many maps); should it not within its bound, false
+// is returned and the caller's results become NaN.
+__device__ __forceinline__ bool cluster_maps_wait(ClusterMaps &m, int step) {
+    const uint32_t bar = smem_addr(&m.bar[step & 1]);
+    for (int polls = 0; polls < (1 << 22); ++polls) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"((uint32_t)(step >> 1) & 1u)
+            : "memory");
+        if (__all_sync(0xffffffffu, done)) return true;
+    }
+    return false;
 }
 
 // Tokens [begin, end) of sequence n among `tokens`: offsets are clamped, so
