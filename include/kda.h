@@ -481,7 +481,7 @@ typedef struct {
 } kda_scan_options;
 
 /* Tokens between the states that kda_gated_scan_fwd saves for the backward pass. */
-#define KDA_SCAN_CARRY_TOKENS 128
+#define KDA_SCAN_CARRY_TOKENS 64
 
 /*
  * Bytes of the `carries` array for these sizes: one row of D fp32 for each of
@@ -505,11 +505,12 @@ size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs);
  *  carries    NULL, or kda_gated_scan_carries_size(...) bytes (written): the
  *             fp32 state entering every KDA_SCAN_CARRY_TOKENS-th token of each
  *             sequence, for kda_gated_scan_bwd. The state entering token
- *             128 i of sequence n, which begins at token s, is row
- *             floor(s / 128) + n + i; other rows are left as they were.
+ *             64 i of sequence n, which begins at token s, is row
+ *             floor(s / 64) + n + i; other rows are left as they were.
  *  dtype, g_dtype: (BF16, BF16), (BF16, F32) or (F32, F32); (F32, BF16)
  *             returns KDA_ERR_UNSUPPORTED
- *  D          channels; a multiple of 4, else KDA_ERR_UNSUPPORTED
+ *  D          channels; a multiple of 8 (of 4 with fp32 x), i.e. rows of whole
+ *             16-byte pieces, else KDA_ERR_UNSUPPORTED
  * Pointers 16-byte aligned (cu_seqlens 4-byte). No workspace. States and sums
  * are fp32; the results do not depend on the run (no atomics).
  */

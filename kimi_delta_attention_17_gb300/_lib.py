@@ -17,7 +17,7 @@ DTYPE_BF16 = 1
 DECAY = {"channel": 0, "scalar": 1, "none": 2}           # kda_decay
 GATE = {"log": 0, "logsigmoid": 1, "bounded": 2}          # kda_gate
 WRITE = {"plain": 0, "complement": 1, "norm": 2}          # kda_write
-SCAN_CARRY_TOKENS = 128                                   # KDA_SCAN_CARRY_TOKENS
+SCAN_CARRY_TOKENS = 64                                    # KDA_SCAN_CARRY_TOKENS
 STATE_COPY_MAX = 4096                                     # KDA_STATE_COPY_MAX
 
 

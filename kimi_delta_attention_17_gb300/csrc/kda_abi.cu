@@ -452,14 +452,14 @@ kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options
     s->T_fixed = T;
     if (s->tokens >= (1LL << 31) - kChunk) return KDA_ERR_INVALID_ARGUMENT;
     if (s->tokens * s->D >= (1LL << 40)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)s->num_seqs * ((s->D + 31) / 32) * 8 >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)s->num_seqs * ((s->D + 31) / 32) * kScanMaxRanks >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
     if (s->tokens > 0 && (!s->x || !s->g)) return KDA_ERR_INVALID_ARGUMENT;
     const void *tensors[] = {s->x,  s->g,  s->dout,        s->init,  s->dfinal, s->out,
                              s->dx, s->dg, s->final_state, s->dinit, s->carries};
     for (const void *p : tensors)
         if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned4(s->cu)) return KDA_ERR_INVALID_ARGUMENT;
-    if (s->D % kScanVec != 0) return KDA_ERR_UNSUPPORTED;
+    if (s->D % (s->dtype == KDA_DTYPE_F32 ? 4 : 8) != 0) return KDA_ERR_UNSUPPORTED;
     if (s->dtype == KDA_DTYPE_F32 && s->g_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
@@ -533,7 +533,7 @@ extern "C" kda_status kda_gated_scan_step(const void *x, const void *g, float *s
     if (N > 0 && (!x || !g || !state || !out)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16(x) || !aligned16(g) || !aligned16(state) || !aligned16(out) || !aligned4(slots))
         return KDA_ERR_INVALID_ARGUMENT;
-    if (D % kScanVec != 0) return KDA_ERR_UNSUPPORTED;
+    if (D % (dtype == KDA_DTYPE_F32 ? 4 : 8) != 0) return KDA_ERR_UNSUPPORTED;
     if (dtype == KDA_DTYPE_F32 && g_dtype != KDA_DTYPE_F32) return KDA_ERR_UNSUPPORTED;
     return launch_scan_step(s, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

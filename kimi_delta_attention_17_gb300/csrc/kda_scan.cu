@@ -22,84 +22,86 @@
 namespace kda {
 namespace {
 
-#ifndef FWD_STAGES
-#define FWD_STAGES 2
-#endif
-struct FwdShared {
-    float map[kScanGroups][2][kScanCh];       // (A, H) of each piece; then H gives way to the state entering it
-    float2 warp_map[2][kScanWarps][kScanCh];  // (A, H) of each warp's tokens
-    ClusterMaps peers;
-};
 template <typename XT, typename GT>
 struct FwdShape {
-    using XP = typename Piece<XT>::type;
-    using GP = typename Piece<GT>::type;
-    static constexpr int stages = FWD_STAGES;
-    static constexpr size_t slots = (size_t)stages * kScanTpt * kScanThreads;
-    static constexpr size_t smem = slots * (sizeof(XP) + sizeof(GP));
-    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(FwdShared) + kCtaReserved));
-    static constexpr int per_sm = kScanTpt == 4 ? (fit < 3 ? fit : 3) : (fit < 4 ? fit : 4);  // CTAs
+    using Tiling = ScanTiling<XT, GT>;
+    static constexpr int threads = kScanThreads, tpt = Tiling::tpt, vec = Tiling::vec, pairs = vec / 2;
+    static constexpr int warps = threads / 32, tile = Tiling::tile, ch = Tiling::ch;
+    using L = typename Lane<ch>::type;
+    using XS = Slots<XT, vec, tpt, threads>;
+    using GS = Slots<GT, vec, tpt, threads>;
+    struct Shared {
+        float map[Tiling::groups][2][ch];  // (A, H) of each group's tokens; then H gives way to the state entering them
+        L warp_map[2][warps][2][32];  // (A, H) of each warp's tokens
+    };
+    static constexpr int stages = 2;
+    static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
+    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
+    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
+    static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
 template <typename XT, typename GT, int kGate, int kWrite>
-__global__ void __launch_bounds__(kScanThreads, FwdShape<XT, GT>::per_sm)
+__global__ void __launch_bounds__(FwdShape<XT, GT>::threads, FwdShape<XT, GT>::per_sm)
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
          float lower) {
     using S = FwdShape<XT, GT>;
-    using XP = typename S::XP;
-    using GP = typename S::GP;
+    using L = typename S::L;
+    using XS = typename S::XS;
+    using GS = typename S::GS;
+    constexpr int V = S::vec, kTpt = S::tpt, kPairs = S::pairs, kTile = S::tile, kWarps = S::warps, kLaneCh = S::ch / 32;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    GP *gs = reinterpret_cast<GP *>(smem_raw);
-    XP *xs = reinterpret_cast<XP *>(smem_raw + S::slots * sizeof(GP));
-    __shared__ __align__(16) FwdShared sh;
+    void *gs = smem_raw;
+    void *xs = smem_raw + S::stages * GS::bytes_per_stage;
+    __shared__ __align__(16) typename S::Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid / kScanLanes;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+    const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
     const int n = (int)(unit / (unsigned)blocks);
-    const int ch0 = (int)(unit % (unsigned)blocks) * kScanCh;
-    const int col = kScanVec * (lane & (kScanLanes - 1));
-    const int ch = ch0 + col;
-    const bool has_ch = ch < D;
-    const int group = tid / kScanLanes;
-    // In every warp, lane = channel: the state at the cluster's next tiles. Read
-    // before the cluster's first barrier: final_state may be the same memory.
-    float carry = init && ch0 + lane < D ? init[(size_t)n * D + ch0 + lane] : 0.f;
-    if (ranks > 1) cluster_maps_init(sh.peers);
+    const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
+    const int col = V * (tid & (kScanLanes - 1));  // this thread's channels, and a lane's where warps compose
+    const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
+
+    // In every warp, by lane: the state at the cluster's next tiles. Read before
+    // the cluster's first barrier: final_state may be the same memory.
+    L carry;
+    lane_set(carry, 0.f);
+    const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
+    if (init && lane_ch) carry = *reinterpret_cast<const L *>(init + state_at);
+    if (ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
     const int len = (int)(end - begin);
-    const int super = kScanTile * ranks;  // tokens per cluster step
+    const int super = kTile * ranks;  // tokens per cluster step
     const int steps = (int)(((long long)len + super - 1) / super);
 
     // Of this step: tokens from this thread's first one to the sequence's end
     // (none left where negative), and the first one's element.
-    int left = has_ch ? len - (rank * kScanTile + group * kScanTpt) : -1;
+    int left = has_ch ? len - (rank * kTile + group * kTpt) : -1;
     const int less = has_ch ? super : 0;
-    size_t at = (size_t)(begin + (long long)rank * kScanTile + group * kScanTpt) * D + ch;
+    size_t at = (size_t)(begin + (long long)rank * kTile + group * kTpt) * D + ch0 + col;
     const size_t stride = (size_t)super * D;
     auto prefetch = [&](int i, int left, size_t from) {
-        const int s0 = i % S::stages * kScanTpt * kScanThreads + tid;
-        const GT *gp = g + from;
-        const XT *xp = x + from;
-        if (left >= kScanTpt) {
+        const int st = i % S::stages;
+        if (left >= kTpt) {
 #pragma unroll
-            for (int j = 0; j < kScanTpt; ++j) {
-                async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], gp + (size_t)j * D);
-                async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], xp + (size_t)j * D);
+            for (int j = 0; j < kTpt; ++j) {
+                GS::copy(gs, st, j, g + from + (size_t)j * D);
+                XS::copy(xs, st, j, x + from + (size_t)j * D);
             }
         } else if (i < steps) {
-            const F2 id = f2(identity_gate<kGate>()), z[2] = {id, id}, zero[2] = {{0}, {0}};
-            for (int j = 0; j < kScanTpt; ++j) {
+            for (int j = 0; j < kTpt; ++j) {
                 if (j < left) {
-                    async_piece<sizeof(GP)>(&gs[s0 + j * kScanThreads], gp + (size_t)j * D);
-                    async_piece<sizeof(XP)>(&xs[s0 + j * kScanThreads], xp + (size_t)j * D);
+                    GS::copy(gs, st, j, g + from + (size_t)j * D);
+                    XS::copy(xs, st, j, x + from + (size_t)j * D);
                 } else {
-                    gs[s0 + j * kScanThreads] = pack4<GT>(z);
-                    xs[s0 + j * kScanThreads] = pack4<XT>(zero);
+                    GS::fill(gs, st, j, identity_gate<kGate>());
+                    XS::fill(xs, st, j, 0.f);
                 }
             }
         }
@@ -110,18 +112,16 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     for (int i = 0; i < S::stages; ++i) prefetch(i, left - i * less, at + i * stride);
     for (int i = 0; i < steps; ++i, at += stride, left -= less) {
         async_wait<S::stages - 1>();
-        const int s0 = i % S::stages * kScanTpt * kScanThreads + tid;
-        F2 a[kScanTpt][kScanPairs], b[kScanTpt][kScanPairs];
+        const int st = i % S::stages;
+        F2 a[kTpt][kPairs], b[kTpt][kPairs];
         {
-            F2 A[kScanPairs], H[kScanPairs] = {{0}, {0}};
-            Decay<kGate> decay[kScanPairs];
+            Pairs<V> H = {};
+            Decay<kGate> decay[kPairs];
 #pragma unroll
-            for (int j = 0; j < kScanTpt; ++j) {
-                F2 xv[kScanPairs], zv[kScanPairs];
-                unpack4(xs[s0 + j * kScanThreads], xv);
-                unpack4(gs[s0 + j * kScanThreads], zv);
+            for (int j = 0; j < kTpt; ++j) {
+                const Pairs<V> xv = XS::get(xs, st, j), zv = GS::get(gs, st, j);
 #pragma unroll
-                for (int c = 0; c < kScanPairs; ++c) {
+                for (int c = 0; c < kPairs; ++c) {
                     const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
                     a[j][c] = q.a;
                     b[j][c] = written<kWrite>(q.a, q.c, xv[c]);
@@ -129,141 +129,127 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
                     decay[c].then(q);
                 }
             }
+            Pairs<V> A;
 #pragma unroll
-            for (int c = 0; c < kScanPairs; ++c) A[c] = decay[c].value();
-            *reinterpret_cast<float4 *>(&sh.map[group][0][col]) = pack4<float>(A);
-            *reinterpret_cast<float4 *>(&sh.map[group][1][col]) = pack4<float>(H);
+            for (int c = 0; c < kPairs; ++c) A[c] = decay[c].value();
+            store_pairs<V>(&sh.map[group][0][col], A);
+            store_pairs<V>(&sh.map[group][1][col], H);
         }
         prefetch(i + S::stages, left - S::stages * less, at + S::stages * stride);  // into the slots just read
-        // Lane = channel: the warp's pieces are composed in order.
         __syncwarp();
-        float A[kWarpGroups], H[kWarpGroups];
+        // By lane: the warp's groups are composed in order.
+        L A[kWarpGroups], H[kWarpGroups];
         {
-            float PA = 1.f, PH = 0.f;
+            L PA, PH;
+            lane_set(PA, 1.f);
+            lane_set(PH, 0.f);
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                A[v] = sh.map[warp * kWarpGroups + v][0][lane];
-                H[v] = sh.map[warp * kWarpGroups + v][1][lane];
+                A[v] = *reinterpret_cast<const L *>(&sh.map[warp * kWarpGroups + v][0][lane * kLaneCh]);
+                H[v] = *reinterpret_cast<const L *>(&sh.map[warp * kWarpGroups + v][1][lane * kLaneCh]);
             }
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                PH = fmaf(A[v], PH, H[v]);
-                PA *= A[v];
+                PH = lane_fma(A[v], PH, H[v]);
+                PA = lane_mul(PA, A[v]);
             }
-            sh.warp_map[i & 1][warp][lane] = make_float2(PA, PH);
+            sh.warp_map[i & 1][warp][0][lane] = PA;
+            sh.warp_map[i & 1][warp][1][lane] = PH;
         }
         __syncthreads();  // warp_map's halves alternate: the only barrier of a step
         {
-            float2 m[kScanWarps];
-#pragma unroll
-            for (int v = 0; v < kScanWarps; ++v) m[v] = sh.warp_map[i & 1][v][lane];
-            float first = carry;  // the state entering the CTA's tile
+            L first = carry;  // the state entering the CTA's tile
             if (ranks > 1) {
                 if (warp == 0) {
-                    float TA = 1.f, TH = 0.f;
+                    L TA, TH;
+                    lane_set(TA, 1.f);
+                    lane_set(TH, 0.f);
 #pragma unroll
-                    for (int v = 0; v < kScanWarps; ++v) {
-                        TH = fmaf(m[v].x, TH, m[v].y);
-                        TA *= m[v].x;
+                    for (int v = 0; v < kWarps; ++v) {
+                        const L WA = sh.warp_map[i & 1][v][0][lane];
+                        TH = lane_fma(WA, TH, sh.warp_map[i & 1][v][1][lane]);
+                        TA = lane_mul(TA, WA);
                     }
-                    cluster_maps_send(sh.peers, i, rank, ranks, TA, TH);
+                    cluster_maps_send(peers, i, TA, TH);
                 }
-                if (!cluster_maps_wait(sh.peers, i)) carry = __uint_as_float(0x7fc00000u);
+                if (!cluster_maps_wait(peers, i)) lane_set(carry, __uint_as_float(0x7fc00000u));
                 for (int r = 0; r < ranks; ++r) {
                     if (r == rank) first = carry;
-                    const float2 t = sh.peers.map[i & 1][r][lane];
-                    carry = fmaf(t.x, carry, t.y);
+                    const auto m = peers.map(i, r);
+                    carry = lane_fma(m.a, carry, m.b);
                 }
             }
-            // The tile begins at a token whose entering state the backward pass needs.
-            const long long tile = (long long)i * ranks + rank;
-            if (carries && warp == 0 && tile * kScanTile < len && ch0 + lane < D)
-                carries[(size_t)carry_row(begin, n, tile) * D + ch0 + lane] = first;
-            float mine = 0.f;  // the state entering the warp's tokens
+            L mine = first;  // the state entering the warp's tokens
 #pragma unroll
-            for (int v = 0; v < kScanWarps; ++v) {
+            for (int v = 0; v < kWarps; ++v) {
                 if (v == warp) mine = first;
-                first = fmaf(m[v].x, first, m[v].y);
+                if (ranks == 1 || v + 1 < kWarps)
+                    first = lane_fma(sh.warp_map[i & 1][v][0][lane], first, sh.warp_map[i & 1][v][1][lane]);
             }
             if (ranks == 1) carry = first;
+            // The states that the backward pass starts its tiles from.
+            const long long t = ((long long)i * ranks + rank) * kTile + warp * kWarpGroups * kTpt;
+            if (carries && t % KDA_SCAN_CARRY_TOKENS == 0 && t < len && lane_ch)
+                *reinterpret_cast<L *>(carries + (size_t)carry_row(begin, n, t / KDA_SCAN_CARRY_TOKENS) * D + ch0 +
+                                       lane * kLaneCh) = mine;
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                sh.map[warp * kWarpGroups + v][1][lane] = mine;
-                mine = fmaf(A[v], mine, H[v]);
+                *reinterpret_cast<L *>(&sh.map[warp * kWarpGroups + v][1][lane * kLaneCh]) = mine;
+                mine = lane_fma(A[v], mine, H[v]);
             }
         }
         __syncwarp();
-        F2 h[kScanPairs];
-        unpack4(*reinterpret_cast<const float4 *>(&sh.map[group][1][col]), h);
+        Pairs<V> h = load_pairs<V>(&sh.map[group][1][col]);
         XT *o = out + at;
 #pragma unroll
-        for (int j = 0; j < kScanTpt; ++j) {
+        for (int j = 0; j < kTpt; ++j) {
 #pragma unroll
-            for (int c = 0; c < kScanPairs; ++c) h[c] = fma2(a[j][c], h[c], b[j][c]);
-            if (j < left) *reinterpret_cast<XP *>(o + (size_t)j * D) = pack4<XT>(h);
+            for (int c = 0; c < kPairs; ++c) h[c] = fma2(a[j][c], h[c], b[j][c]);
+            if (j < left) store_pairs<V>(o + (size_t)j * D, h);
         }
     }
     async_wait<0>();
-    if (final_state && warp == 0 && rank == 0 && ch0 + lane < D) final_state[(size_t)n * D + ch0 + lane] = carry;
+    if (final_state && warp == 0 && rank == 0 && lane_ch) *reinterpret_cast<L *>(final_state + state_at) = carry;
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
-    using S = FwdShape<XT, GT>;
-    auto kernel = scan_fwd<XT, GT, kGate, kWrite>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
-    if (err != cudaSuccess) return err;
-    const int blocks = (s.D + kScanCh - 1) / kScanCh;
-    const long long units = (long long)s.num_seqs * blocks;
-    const int ranks = scan_ranks(units, s.cu ? s.tokens : s.T_fixed, 152 * S::per_sm);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * ranks));
-    cfg.blockDim = dim3(kScanThreads);
-    cfg.dynamicSmemBytes = S::smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), s.init,
-                              s.cu, static_cast<XT *>(s.out), s.final_state, s.carries, s.T_fixed, s.tokens,
-                              s.D, blocks, ranks, s.gate.lower);
+    return launch_scan<FwdShape<XT, GT>, scan_fwd<XT, GT, kGate, kWrite>>(
+        s, stream, static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), s.init, s.cu, static_cast<XT *>(s.out),
+        s.final_state, s.carries, s.T_fixed, s.tokens, s.D);
 }
 
-// One step: a thread per four channels of a row.
+// One step: a thread per 16-byte piece of g.
 constexpr int kStepThreads = 128;
 template <typename XT, typename GT, int kGate, int kWrite>
 __global__ void __launch_bounds__(kStepThreads)
 scan_step(const XT *__restrict__ x, const GT *__restrict__ g, float *__restrict__ state,
           const int32_t *__restrict__ slots, XT *__restrict__ out, long long pieces, int per_row, int num_slots,
           float lower) {
+    constexpr int V = kVec<GT>;
     const long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x;
     if (i >= pieces) return;
-    const int n = (int)(i / per_row), c4 = (int)(i % per_row);
+    const int n = (int)(i / per_row), c = (int)(i % per_row) * V;
     const long long slot = slots ? slots[n] : n;
-    const size_t at = (size_t)i * kScanVec;
-    F2 h[kScanPairs] = {{0}, {0}};
+    const size_t at = (size_t)i * V;
+    Pairs<V> h = {};
     if (slot >= 0 && slot < num_slots) {
-        F2 xv[kScanPairs], zv[kScanPairs];
-        float4 *sp = reinterpret_cast<float4 *>(state) + (size_t)slot * per_row + c4;
-        unpack4(*sp, h);
-        unpack4(*reinterpret_cast<const typename Piece<XT>::type *>(x + at), xv);
-        unpack4(*reinterpret_cast<const typename Piece<GT>::type *>(g + at), zv);
+        float *sp = state + (size_t)slot * per_row * V + c;
+        h = load_pairs<V>(sp);
+        const Pairs<V> xv = load_pairs<V>(x + at), zv = load_pairs<V>(g + at);
 #pragma unroll
-        for (int c = 0; c < kScanPairs; ++c) {
+        for (int c = 0; c < V / 2; ++c) {
             const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
             h[c] = fma2(q.a, h[c], written<kWrite>(q.a, q.c, xv[c]));
         }
-        *sp = pack4<float>(h);
+        store_pairs<V>(sp, h);
     }
-    *reinterpret_cast<typename Piece<XT>::type *>(out + at) = pack4<XT>(h);
+    store_pairs<V>(out + at, h);
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_step(const ScanStepArgs &s, cudaStream_t stream) {
-    const int per_row = s.D / kScanVec;
+    const int per_row = s.D / kVec<GT>;
     const long long pieces = (long long)s.N * per_row;
     const long long grid = (pieces + kStepThreads - 1) / kStepThreads;
     scan_step<XT, GT, kGate, kWrite><<<(unsigned)grid, kStepThreads, 0, stream>>>(

@@ -1,13 +1,13 @@
 // Shared by the gated linear recurrence's kernels (h_t = a_t h_{t-1} + w_t x_t):
-// the gate functions, four-channel pieces, and the composition of affine maps.
+// the gate functions, 16-byte pieces, and the exchange of affine maps.
 #pragma once
 
-#include <stdlib.h>
+#include <atomic>
+
 #include "kda_internal.cuh"
 
 namespace kda {
 
-constexpr int kScanVec = 4;  // channels per thread: 8 bytes of bf16, 16 of fp32
 
 // Validated kda_scan_options.
 struct ScanGate {
@@ -188,59 +188,144 @@ struct Decay<KDA_GATE_LOGSIGMOID> {
     }
 };
 
-// Four values as they lie in memory.
-template <typename T> struct Piece;
-template <> struct Piece<float> { using type = float4; };
-template <> struct Piece<__nv_bfloat16> { using type = uint2; };
+// A thread holds the channels of one 16-byte piece of g: eight of bf16, four of
+// fp32. Rows of 64 bytes cost bandwidth (copies alone, measured: 3.4 TB/s in
+// 8-byte pieces of 64-byte rows, 6.5 TB/s in 16-byte pieces of 128-byte rows),
+// so it is the wider operand that gets the 128 bytes.
+template <typename GT>
+constexpr int kVec = 16 / (int)sizeof(GT);
 
-__device__ __forceinline__ void unpack4(const float4 &r, F2 *x) {
-    x[0] = f2(r.x, r.y);
-    x[1] = f2(r.z, r.w);
+template <int kBytes> struct PieceOf { using type = uint4; };
+template <> struct PieceOf<8> { using type = uint2; };
+template <typename T, int V>
+using Piece = typename PieceOf<V *(int)sizeof(T)>::type;  // V values of T: 8 or 16 bytes
+
+// V values of one token, as pairs.
+template <int V>
+struct Pairs {
+    F2 v[V / 2];
+    __device__ __forceinline__ F2 &operator[](int i) { return v[i]; }
+    __device__ __forceinline__ const F2 &operator[](int i) const { return v[i]; }
+};
+__device__ __forceinline__ F2 unpack2(uint32_t u) {
+    return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack4(const uint2 &r, F2 *x) {
-    x[0] = f2(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u));
-    x[1] = f2(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u));
+__device__ __forceinline__ uint32_t pack2(F2 x) {
+    float lo, hi;
+    split(x, lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
-template <typename T> __device__ __forceinline__ typename Piece<T>::type pack4(const F2 *x);
-template <> __device__ __forceinline__ float4 pack4<float>(const F2 *x) {
-    float4 r;
-    split(x[0], r.x, r.y);
-    split(x[1], r.z, r.w);
-    return r;
+template <typename T, int V> struct Convert;
+template <> struct Convert<float, 4> {
+    static __device__ __forceinline__ void unpack(const uint4 &r, F2 *x) {
+        x[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+        x[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 *x) {
+        float v[4];
+        split(x[0], v[0], v[1]);
+        split(x[1], v[2], v[3]);
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+};
+template <> struct Convert<__nv_bfloat16, 4> {
+    static __device__ __forceinline__ void unpack(const uint2 &r, F2 *x) {
+        x[0] = unpack2(r.x);
+        x[1] = unpack2(r.y);
+    }
+    static __device__ __forceinline__ uint2 pack(const F2 *x) { return make_uint2(pack2(x[0]), pack2(x[1])); }
+};
+template <> struct Convert<__nv_bfloat16, 8> {
+    static __device__ __forceinline__ void unpack(const uint4 &r, F2 *x) {
+        x[0] = unpack2(r.x);
+        x[1] = unpack2(r.y);
+        x[2] = unpack2(r.z);
+        x[3] = unpack2(r.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const F2 *x) {
+        return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
+    }
+};
+template <int V>
+__device__ __forceinline__ Pairs<V> load_pairs(const __nv_bfloat16 *from) {
+    Pairs<V> x;
+    Convert<__nv_bfloat16, V>::unpack(*reinterpret_cast<const Piece<__nv_bfloat16, V> *>(from), x.v);
+    return x;
 }
-template <> __device__ __forceinline__ uint2 pack4<__nv_bfloat16>(const F2 *x) {
-    const float4 r = pack4<float>(x);
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(r.x, r.y), hi = __floats2bfloat162_rn(r.z, r.w);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+template <int V>
+__device__ __forceinline__ void store_pairs(__nv_bfloat16 *to, const Pairs<V> &x) {
+    *reinterpret_cast<Piece<__nv_bfloat16, V> *>(to) = Convert<__nv_bfloat16, V>::pack(x.v);
+}
+template <int V>
+__device__ __forceinline__ Pairs<V> load_pairs(const float *from) {
+    Pairs<V> x;
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) Convert<float, 4>::unpack(reinterpret_cast<const uint4 *>(from)[q], &x.v[2 * q]);
+    return x;
+}
+template <int V>
+__device__ __forceinline__ void store_pairs(float *to, const Pairs<V> &x) {
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) reinterpret_cast<uint4 *>(to)[q] = Convert<float, 4>::pack(&x.v[2 * q]);
 }
 
-// The tiling that the forward and the backward scan share.
-constexpr int kScanPairs = kScanVec / 2;
-constexpr int kScanLanes = 8;                         // threads across the channels
-constexpr int kScanCh = kScanLanes * kScanVec;        // channels per CTA
-#ifndef SCAN_THREADS
-#define SCAN_THREADS 128
-#endif
-constexpr int kScanThreads = SCAN_THREADS;
-constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanGroups = kScanThreads / kScanLanes;  // pieces of consecutive tokens per tile
-constexpr int kWarpGroups = 32 / kScanLanes;            // and per warp
-constexpr int kScanTpt = 128 / kScanGroups;                           // tokens per thread
-constexpr int kScanTile = kScanGroups * kScanTpt;
+// The tiling that the forward and the backward scan share: 8 threads span the
+// pieces of a row's block of channels, a warp four groups of consecutive
+// tokens, a CTA 16. 32 values a thread, 16 where all of them are fp32 and arrive
+// in twice the bytes (chosen by measurement, GB300: 128 threads against 256, 4
+// tokens against 8, each within 3 % of the best or better on every workload).
+constexpr int kScanThreads = 128;
+constexpr int kScanLanes = 8;                 // threads across the channels
+constexpr int kWarpGroups = 32 / kScanLanes;  // groups per warp
+template <typename XT, typename GT>
+struct ScanTiling {
+    static constexpr int vec = kVec<GT>;                              // channels per thread
+    static constexpr int tpt = sizeof(XT) < sizeof(GT) ? 8 : 4;       // tokens per thread
+    static constexpr int groups = kScanThreads / kScanLanes, tile = groups * tpt;
+    static constexpr int ch = kScanLanes * vec;                       // channels per CTA
+};
+constexpr int kScanMaxRanks = 16;
 constexpr size_t kSmSmem = 228 * 1024, kCtaReserved = 1024;  // shared memory of an SM, and what each CTA takes beside its own
-constexpr int kScanMaxRanks = 8;
-static_assert(kScanTile == KDA_SCAN_CARRY_TOKENS, "a tile begins at a saved state");
-static_assert(kScanCh == 32, "one lane per channel composes a tile's maps");
 
-// Copies one piece to shared memory without passing through registers.
-template <int kBytes>
-__device__ __forceinline__ void async_piece(void *smem, const void *gmem) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(smem);
-    if (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(gmem) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(gmem) : "memory");
-}
+// The slots of shared memory that a thread's tokens arrive in, [stage][token of
+// the thread][thread]: each thread copies what it reads itself.
+template <typename T, int V, int kTpt, int kThreads>
+struct Slots {
+    using P = Piece<T, V>;
+    static constexpr size_t bytes_per_stage = (size_t)kTpt * kThreads * sizeof(P);
+    static __device__ __forceinline__ P *at(void *base, int stage, int j) {
+        return static_cast<P *>(base) + (stage * kTpt + j) * kThreads + threadIdx.x;
+    }
+    static __device__ __forceinline__ void copy(void *base, int stage, int j, const T *from) {
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(at(base, stage, j));
+        if (sizeof(P) == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(from) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(from) : "memory");
+    }
+    static __device__ __forceinline__ void fill(void *base, int stage, int j, float value) {
+        const F2 v[4] = {f2(value), f2(value), f2(value), f2(value)};
+        *at(base, stage, j) = Convert<T, V>::pack(v);
+    }
+    static __device__ __forceinline__ Pairs<V> get(void *base, int stage, int j) {
+        Pairs<V> x;
+        Convert<T, V>::unpack(*at(base, stage, j), x.v);
+        return x;
+    }
+};
+
+// Where whole warps compose maps, a lane holds a block's channels / 32: one fp32
+// value, or a pair.
+template <int kCh> struct Lane { using type = F2; };
+template <> struct Lane<32> { using type = float; };
+__device__ __forceinline__ float lane_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 lane_fma(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float lane_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ F2 lane_mul(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ void lane_set(float &x, float v) { x = v; }
+__device__ __forceinline__ void lane_set(F2 &x, float v) { x = f2(v); }
+
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void async_wait() {
@@ -257,18 +342,29 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // The exchange of tile maps between the CTAs of a cluster. Each step every CTA
-// sends its map (two floats per channel) to every CTA, itself included, by
+// sends its map (two values per channel) to every CTA, itself included, by
 // asynchronous stores that the receiver's mbarrier counts: no fence, which
 // would wait for the outputs on their way to memory. Buffers alternate between
 // steps: a CTA sends step i + 2 only after it has everyone's maps of step
 // i + 1, which each sends after a CTA barrier that follows its reads of step i.
+template <int kCh>
 struct ClusterMaps {
-    float2 map[2][kScanMaxRanks][kScanCh];
-    unsigned long long bar[2];
+    using L = typename Lane<kCh>::type;
+    struct __align__(2 * sizeof(L)) Map {
+        L a, b;
+    };
+    // In shared memory: two mbarriers, then [2][ranks][32] maps.
+    static constexpr size_t bytes(int ranks) { return ranks > 1 ? 16 + 2 * ranks * 32 * sizeof(Map) : 0; }
+    unsigned long long *bar;
+    int rank, ranks;
+    __device__ __forceinline__ Map &map(int step, int r) const {
+        return reinterpret_cast<Map *>(bar + 2)[((step & 1) * ranks + r) * 32 + (threadIdx.x & 31)];
+    }
 };
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // All threads of the cluster, once.
-__device__ __forceinline__ void cluster_maps_init(ClusterMaps &m) {
+template <int kCh>
+__device__ __forceinline__ void cluster_maps_init(const ClusterMaps<kCh> &m) {
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&m.bar[b])) : "memory");
@@ -276,27 +372,37 @@ __device__ __forceinline__ void cluster_maps_init(ClusterMaps &m) {
     }
     cluster_sync();
 }
-// One warp, lane = channel: sends (a, b) as step `step`'s map of this CTA.
-__device__ __forceinline__ void cluster_maps_send(ClusterMaps &m, int step, int rank, int ranks, float a, float b) {
-    const int lane = threadIdx.x & 31, p = step & 1;
-    const uint32_t bar = smem_addr(&m.bar[p]), mine = smem_addr(&m.map[p][rank][lane]);
-    if (lane == 0)
+__device__ __forceinline__ void send_async(uint32_t to, uint32_t bar, float a, float b) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(a),
+                 "f"(b), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send_async(uint32_t to, uint32_t bar, F2 a, F2 b) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(to),
+                 "l"(a.v), "l"(b.v), "r"(bar)
+                 : "memory");
+}
+// One warp: sends (a, b) as step `step`'s map of this CTA.
+template <int kCh>
+__device__ __forceinline__ void cluster_maps_send(const ClusterMaps<kCh> &m, int step, typename Lane<kCh>::type a,
+                                                  typename Lane<kCh>::type b) {
+    const uint32_t bar = smem_addr(&m.bar[step & 1]), mine = smem_addr(&m.map(step, m.rank));
+    if ((threadIdx.x & 31) == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                     "r"(ranks * kScanCh * (int)sizeof(float2))
+                     "r"(m.ranks * 32 * (int)sizeof(typename ClusterMaps<kCh>::Map))
                      : "memory");
-    for (int r = 0; r < ranks; ++r) {
+    for (int r = 0; r < m.ranks; ++r) {
         uint32_t to, to_bar;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(r));
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
-        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to),
-                     "f"(a), "f"(b), "r"(to_bar)
-                     : "memory");
+        send_async(to, to_bar, a, b);
     }
 }
 // Waits for the maps of step `step`. The wait always ends (the CTAs of a cluster
 // run together and send as many maps); should it not within its bound, false
 // is returned and the caller's results become NaN.
-__device__ __forceinline__ bool cluster_maps_wait(ClusterMaps &m, int step) {
+template <int kCh>
+__device__ __forceinline__ bool cluster_maps_wait(const ClusterMaps<kCh> &m, int step) {
     const uint32_t bar = smem_addr(&m.bar[step & 1]);
     for (int polls = 0; polls < (1 << 22); ++polls) {
         uint32_t done;
@@ -358,14 +464,72 @@ struct ScanStepArgs {
 };
 cudaError_t launch_scan_step(const ScanStepArgs &s, cudaStream_t stream);
 
-// CTAs per cluster, i.e. tiles of one (sequence, channel block) in flight at
-// once: as many as still run all at the same time (`slots` CTAs fit the GPU),
-// up to the tiles that the longest sequence can have.
-inline int scan_ranks(long long units, long long longest, long long slots) {
-    if (const char *e = getenv("KDA_RANKS")) return atoi(e);
-    int ranks = 1;
-    while (ranks < kScanMaxRanks && 2 * ranks * units <= slots && (long long)ranks * kScanTile < longest) ranks *= 2;
-    return ranks;
+// What one scan kernel needs to know of a device, looked up on first use: how
+// many clusters of each size run at the same time.
+struct ScanFits {
+    static constexpr int kDevices = 64;
+    std::atomic<int> clusters[kDevices][kScanMaxRanks + 1];  // 0: not looked up
+    std::atomic<bool> ready[kDevices];                       // the kernel's attributes are set
+};
+
+// Launches a scan over the (sequence, channel block) pairs. CTAs per cluster:
+// as many as still let all clusters run at the same time, up to the tiles that
+// the longest sequence can have (bf16 backward of 32 pairs of 16384 tokens:
+// 420 us with 1, 123 with 4, 88 with 8, the most that fit, 126 with 9). Where
+// not even two do, up to 4 as long as that makes no more than five rounds of
+// CTAs: several rounds of short ones leave the SMs less unevenly loaded than
+// one of long ones (512 pairs of 4096 tokens: 230 us with 2, 193 with 4).
+template <typename S, auto kKernel, typename... A>
+cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
+    static ScanFits fits;  // one for each kernel
+    const auto kernel = kKernel;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev >= ScanFits::kDevices) return cudaErrorInvalidDevice;
+    if (!fits.ready[dev].load(std::memory_order_acquire)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)(S::smem + ClusterMaps<S::ch>::bytes(kScanMaxRanks)));
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+        fits.ready[dev].store(true, std::memory_order_release);
+    }
+    const int blocks = (s.D + S::ch - 1) / S::ch;
+    const long long units = (long long)s.num_seqs * blocks;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(S::threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto shape = [&](int ranks) {
+        attr[0].val.clusterDim.x = ranks;
+        cfg.gridDim = dim3((unsigned)(units * ranks));
+        cfg.dynamicSmemBytes = S::smem + ClusterMaps<S::ch>::bytes(ranks);
+    };
+    auto fit = [&](int ranks) {  // clusters of this size at the same time
+        int n = fits.clusters[dev][ranks].load(std::memory_order_relaxed);
+        if (n > 0) return n;
+        shape(ranks);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) err = e;
+        n = n > 0 ? n : 1;
+        if (e == cudaSuccess) fits.clusters[dev][ranks].store(n, std::memory_order_relaxed);
+        return n;
+    };
+    const long long longest = s.cu ? s.tokens : s.T_fixed;
+    int ranks = kScanMaxRanks;
+    while (ranks > 1 && ((long long)(ranks - 1) * S::tile >= longest || fit(ranks) < units)) --ranks;
+    if (ranks == 1 && units > fit(2)) {
+        const long long mean = s.tokens / s.num_seqs;
+        ranks = 4;
+        while (ranks > 1 && (ranks * units > 5LL * fit(1) || ranks * S::tile > mean)) ranks /= 2;
+    }
+    if (err != cudaSuccess) return err;
+    shape(ranks);
+    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, s.gate.lower);
 }
 
 // fn<storage type, gate type, gate, write>(args, stream) for a checked call.

@@ -7,8 +7,7 @@
 // a cluster of CTAs over consecutive tiles, which here goes through the
 // sequence from its end. dg needs h_{t-1} as well; it is formed again within
 // the tile by the forward composition, from the fp32 state that the forward
-// call saved at the tile's first token (a tile is KDA_SCAN_CARRY_TOKENS
-// tokens), so neither h nor a second pass over the sequence is read, and h is
+// call saved at the tile's first token, so neither h nor a second pass over the sequence is read, and h is
 // not taken from its rounded outputs. Bound by HBM: x, g and dout in, dx and
 // dg out, once each.
 #include "kda_scan.cuh"
@@ -16,119 +15,121 @@
 namespace kda {
 namespace {
 
-#ifndef BWD_STAGES
-#define BWD_STAGES 2
-#endif
-struct BwdShared {
-    float map[kScanGroups][3][kScanCh];          // A, H, U of each piece; then the state and the gradient entering it
-    float warp_map[2][3][kScanWarps][kScanCh];   // A, H, U of each warp's tokens
-    ClusterMaps peers;
-};
 template <typename XT, typename GT>
 struct BwdShape {
-    using XP = typename Piece<XT>::type;
-    using GP = typename Piece<GT>::type;
-    static constexpr int stages = BWD_STAGES;
-    static constexpr size_t slots = (size_t)stages * kScanTpt * kScanThreads;
-    static constexpr size_t smem = slots * (2 * sizeof(XP) + sizeof(GP));
-    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(BwdShared) + kCtaReserved));
-    static constexpr int per_sm = kScanTpt == 4 ? (fit < 3 ? fit : 3) : (fit < 4 ? fit : 4);  // CTAs
+    using Tiling = ScanTiling<XT, GT>;
+    static constexpr int threads = kScanThreads, tpt = Tiling::tpt, vec = Tiling::vec, pairs = vec / 2;
+    static constexpr int warps = threads / 32, tile = Tiling::tile, ch = Tiling::ch;
+    static_assert(tile % KDA_SCAN_CARRY_TOKENS == 0, "a tile begins at a saved state");
+    using L = typename Lane<ch>::type;
+    using XS = Slots<XT, vec, tpt, threads>;
+    using GS = Slots<GT, vec, tpt, threads>;
+    struct Shared {
+        float map[Tiling::groups][3][ch];     // A, H, U of each group's tokens; then the state and the gradient entering them
+        L warp_map[2][warps][3][32];  // A, H, U of each warp's tokens
+    };
+    static constexpr int stages = 2;
+    static constexpr size_t smem = stages * (2 * XS::bytes_per_stage + GS::bytes_per_stage);
+    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
+    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
+    static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
 template <typename XT, typename GT, int kGate, int kWrite>
-__global__ void __launch_bounds__(kScanThreads, BwdShape<XT, GT>::per_sm)
+__global__ void __launch_bounds__(BwdShape<XT, GT>::threads, BwdShape<XT, GT>::per_sm)
 scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict__ x,
          const GT *__restrict__ g, const float *__restrict__ carries, const int32_t *__restrict__ cu,
          XT *__restrict__ dx, GT *__restrict__ dg, float *dinit, int T_fixed, long long tokens, int D,
          int blocks, int ranks, float lower) {
     using S = BwdShape<XT, GT>;
-    using XP = typename S::XP;
-    using GP = typename S::GP;
+    using L = typename S::L;
+    using XS = typename S::XS;
+    using GS = typename S::GS;
+    constexpr int V = S::vec, kTpt = S::tpt, kPairs = S::pairs, kTile = S::tile, kWarps = S::warps, kLaneCh = S::ch / 32;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    GP *gs = reinterpret_cast<GP *>(smem_raw);
-    XP *xs = reinterpret_cast<XP *>(smem_raw + S::slots * sizeof(GP));
-    XP *ds = xs + S::slots;
-    __shared__ __align__(16) BwdShared sh;
+    void *gs = smem_raw;
+    void *xs = smem_raw + S::stages * GS::bytes_per_stage;
+    void *ds = smem_raw + S::stages * (GS::bytes_per_stage + XS::bytes_per_stage);
+    __shared__ __align__(16) typename S::Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid / kScanLanes;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+    const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;
     const int n = (int)(unit / (unsigned)blocks);
-    const int ch0 = (int)(unit % (unsigned)blocks) * kScanCh;
-    const int col = kScanVec * (lane & (kScanLanes - 1));
-    const int ch = ch0 + col;
-    const bool has_ch = ch < D, lane_ch = ch0 + lane < D;
-    const int group = tid / kScanLanes;
-    // In every warp, lane = channel: the gradient entering the cluster's tiles
-    // from behind. Read before the cluster's first barrier: dinit may be the
-    // same memory.
-    float u = dfinal && lane_ch ? dfinal[(size_t)n * D + ch0 + lane] : 0.f;
-    if (ranks > 1) cluster_maps_init(sh.peers);
+    const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
+    const int col = V * (tid & (kScanLanes - 1));
+    const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
+
+    // In every warp, by lane: the gradient entering the cluster's tiles from
+    // behind. Read before the cluster's first barrier: dinit may be the same
+    // memory.
+    L u;
+    lane_set(u, 0.f);
+    const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
+    if (dfinal && lane_ch) u = *reinterpret_cast<const L *>(dfinal + state_at);
+    if (ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
     const int len = (int)(end - begin);
-    const int super = kScanTile * ranks;
+    const int super = kTile * ranks;
     const int steps = (int)(((long long)len + super - 1) / super);
 
     // Of a step: tokens from this thread's first one to the sequence's end (none
     // left where negative), and the first one's element.
-    const long long t0 = ((long long)(steps - 1) * ranks + rank) * kScanTile + group * kScanTpt;
+    const long long t0 = ((long long)(steps - 1) * ranks + rank) * kTile + group * kTpt;
     int left = has_ch ? (int)(len - t0) : -1;
     const int more = has_ch ? super : 0;
-    size_t at = (size_t)(begin + t0) * D + ch;
+    size_t at = (size_t)(begin + t0) * D + ch0 + col;
     const size_t stride = (size_t)super * D;
     auto prefetch = [&](int i, int left, size_t from) {
-        const int s0 = (i + S::stages) % S::stages * kScanTpt * kScanThreads + tid;
-        const GT *gp = g + from;
-        const XT *xp = x + from, *dp = dout + from;
-        if (i >= 0 && left >= kScanTpt) {
+        const int st = i & 1;
+        if (i >= 0 && left >= kTpt) {
 #pragma unroll
-            for (int j = 0; j < kScanTpt; ++j) {
-                const int s = s0 + j * kScanThreads;
-                async_piece<sizeof(GP)>(&gs[s], gp + (size_t)j * D);
-                async_piece<sizeof(XP)>(&ds[s], dp + (size_t)j * D);
-                async_piece<sizeof(XP)>(&xs[s], xp + (size_t)j * D);
+            for (int j = 0; j < kTpt; ++j) {
+                GS::copy(gs, st, j, g + from + (size_t)j * D);
+                XS::copy(ds, st, j, dout + from + (size_t)j * D);
+                XS::copy(xs, st, j, x + from + (size_t)j * D);
             }
         } else if (i >= 0) {
-            const F2 id = f2(identity_gate<kGate>()), z[2] = {id, id}, zero[2] = {{0}, {0}};
-            for (int j = 0; j < kScanTpt; ++j) {
-                const int s = s0 + j * kScanThreads;
+            for (int j = 0; j < kTpt; ++j) {
                 if (j < left) {
-                    async_piece<sizeof(GP)>(&gs[s], gp + (size_t)j * D);
-                    async_piece<sizeof(XP)>(&ds[s], dp + (size_t)j * D);
-                    async_piece<sizeof(XP)>(&xs[s], xp + (size_t)j * D);
+                    GS::copy(gs, st, j, g + from + (size_t)j * D);
+                    XS::copy(ds, st, j, dout + from + (size_t)j * D);
+                    XS::copy(xs, st, j, x + from + (size_t)j * D);
                 } else {
-                    gs[s] = pack4<GT>(z);
-                    ds[s] = xs[s] = pack4<XT>(zero);
+                    GS::fill(gs, st, j, identity_gate<kGate>());
+                    XS::fill(ds, st, j, 0.f);
+                    XS::fill(xs, st, j, 0.f);
                 }
             }
         }
         async_commit();
     };
 
-#pragma unroll
-    for (int i = 1; i < S::stages; ++i) prefetch(steps - i, left + (i - 1) * more, at - (i - 1) * stride);
+    prefetch(steps - 1, left, at);
     for (int i = steps - 1; i >= 0; --i, at -= stride, left += more) {
-        const int s0 = i % S::stages * kScanTpt * kScanThreads + tid, p = i & 1;
-        const long long tile = (long long)i * ranks + rank;
-        float h0 = 0.f;  // lane = channel: the state entering this CTA's tile
-        if (lane_ch && tile * kScanTile < len) h0 = carries[(size_t)carry_row(begin, n, tile) * D + ch0 + lane];
-        prefetch(i - (S::stages - 1), left + (S::stages - 1) * more, at - (S::stages - 1) * stride);
-        async_wait<S::stages - 1>();
+        const int st = i & 1, p = i & 1;
+        const long long tile = ((long long)i * ranks + rank) * kTile;  // the CTA's first token
+        L h0;  // by lane: the state entering it
+        lane_set(h0, 0.f);
+        if (lane_ch && tile < len)
+            h0 = *reinterpret_cast<const L *>(carries + (size_t)carry_row(begin, n, tile / KDA_SCAN_CARRY_TOKENS) * D + ch0 +
+                                              lane * kLaneCh);
+        prefetch(i - 1, left + more, at - stride);
+        async_wait<1>();
         // c = 1 - a is kept where the slopes need it.
         constexpr bool kKeepC = kGate == KDA_GATE_LOGSIGMOID || kWrite != KDA_WRITE_PLAIN;
-        F2 a[kScanTpt][kScanPairs], b[kScanTpt][kScanPairs], c1[kKeepC ? kScanTpt : 1][kScanPairs];
+        F2 a[kTpt][kPairs], b[kTpt][kPairs], c1[kKeepC ? kTpt : 1][kPairs];
         {
-            F2 A[kScanPairs], H[kScanPairs] = {{0}, {0}}, U[kScanPairs] = {{0}, {0}};
-            Decay<kGate> decay[kScanPairs];
+            Pairs<V> A, H = {}, U = {};
+            Decay<kGate> decay[kPairs];
 #pragma unroll
-            for (int j = 0; j < kScanTpt; ++j) {
-                F2 xv[kScanPairs], zv[kScanPairs];
-                unpack4(xs[s0 + j * kScanThreads], xv);
-                unpack4(gs[s0 + j * kScanThreads], zv);
+            for (int j = 0; j < kTpt; ++j) {
+                const Pairs<V> xv = XS::get(xs, st, j), zv = GS::get(gs, st, j);
 #pragma unroll
-                for (int c = 0; c < kScanPairs; ++c) {
+                for (int c = 0; c < kPairs; ++c) {
                     const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
                     a[j][c] = q.a;
                     if (kKeepC) c1[kKeepC ? j : 0][c] = q.c;
@@ -138,96 +139,92 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                 }
             }
 #pragma unroll
-            for (int j = kScanTpt - 1; j >= 0; --j) {
-                F2 dv[kScanPairs];
-                unpack4(ds[s0 + j * kScanThreads], dv);
+            for (int j = kTpt - 1; j >= 0; --j) {
+                const Pairs<V> dv = XS::get(ds, st, j);
 #pragma unroll
-                for (int c = 0; c < kScanPairs; ++c) U[c] = mul2(a[j][c], add2(dv[c], U[c]));
+                for (int c = 0; c < kPairs; ++c) U[c] = mul2(a[j][c], add2(dv[c], U[c]));
             }
 #pragma unroll
-            for (int c = 0; c < kScanPairs; ++c) A[c] = decay[c].value();
-            *reinterpret_cast<float4 *>(&sh.map[group][0][col]) = pack4<float>(A);
-            *reinterpret_cast<float4 *>(&sh.map[group][1][col]) = pack4<float>(H);
-            *reinterpret_cast<float4 *>(&sh.map[group][2][col]) = pack4<float>(U);
+            for (int c = 0; c < kPairs; ++c) A[c] = decay[c].value();
+            store_pairs<V>(&sh.map[group][0][col], A);
+            store_pairs<V>(&sh.map[group][1][col], H);
+            store_pairs<V>(&sh.map[group][2][col], U);
         }
         __syncwarp();
-        float A[kWarpGroups], H[kWarpGroups], U[kWarpGroups];
+        auto entry = [&](int v, int k) -> L & {
+            return *reinterpret_cast<L *>(&sh.map[warp * kWarpGroups + v][k][lane * kLaneCh]);
+        };
+        L A[kWarpGroups], H[kWarpGroups], U[kWarpGroups];
         {
-            float PA = 1.f, PH = 0.f, QU = 0.f;
+            L PA, PH, QU;
+            lane_set(PA, 1.f);
+            lane_set(PH, 0.f);
+            lane_set(QU, 0.f);
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                A[v] = sh.map[warp * kWarpGroups + v][0][lane];
-                H[v] = sh.map[warp * kWarpGroups + v][1][lane];
-                U[v] = sh.map[warp * kWarpGroups + v][2][lane];
+                A[v] = entry(v, 0);
+                H[v] = entry(v, 1);
+                U[v] = entry(v, 2);
             }
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                PH = fmaf(A[v], PH, H[v]);
-                PA *= A[v];
-                QU = fmaf(A[kWarpGroups - 1 - v], QU, U[kWarpGroups - 1 - v]);
+                PH = lane_fma(A[v], PH, H[v]);
+                PA = lane_mul(PA, A[v]);
+                QU = lane_fma(A[kWarpGroups - 1 - v], QU, U[kWarpGroups - 1 - v]);
             }
-            sh.warp_map[p][0][warp][lane] = PA;
-            sh.warp_map[p][1][warp][lane] = PH;
-            sh.warp_map[p][2][warp][lane] = QU;
+            sh.warp_map[p][warp][0][lane] = PA;
+            sh.warp_map[p][warp][1][lane] = PH;
+            sh.warp_map[p][warp][2][lane] = QU;
         }
         __syncthreads();  // warp_map's halves alternate: the only barrier of a step
         {
-            float WA[kScanWarps], WU[kScanWarps];
-#pragma unroll
-            for (int v = 0; v < kScanWarps; ++v) {
-                WA[v] = sh.warp_map[p][0][v][lane];
-                WU[v] = sh.warp_map[p][2][v][lane];
-            }
             if (ranks > 1 && warp == 0) {
-                float TA = 1.f, TU = 0.f;
+                L TA, TU;
+                lane_set(TA, 1.f);
+                lane_set(TU, 0.f);
 #pragma unroll
-                for (int v = kScanWarps - 1; v >= 0; --v) {
-                    TU = fmaf(WA[v], TU, WU[v]);
-                    TA *= WA[v];
+                for (int v = kWarps - 1; v >= 0; --v) {
+                    const L WA = sh.warp_map[p][v][0][lane];
+                    TU = lane_fma(WA, TU, sh.warp_map[p][v][2][lane]);
+                    TA = lane_mul(TA, WA);
                 }
-                cluster_maps_send(sh.peers, steps - 1 - i, rank, ranks, TA, TU);
+                cluster_maps_send(peers, steps - 1 - i, TA, TU);
             }
-            float mine = 0.f;  // the state entering the warp's tokens
-#pragma unroll
-            for (int v = 0; v < kScanWarps; ++v) {
-                if (v == warp) mine = h0;
-                h0 = fmaf(WA[v], h0, sh.warp_map[p][1][v][lane]);
-            }
+            for (int v = 0; v < warp; ++v) h0 = lane_fma(sh.warp_map[p][v][0][lane], h0, sh.warp_map[p][v][1][lane]);
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
-                sh.map[warp * kWarpGroups + v][1][lane] = mine;
-                mine = fmaf(A[v], mine, H[v]);
+                entry(v, 1) = h0;
+                h0 = lane_fma(A[v], h0, H[v]);
             }
-            float last = u;  // the gradient entering the CTA's tile from behind
+            L last = u;  // the gradient entering the CTA's tile from behind
             if (ranks > 1) {
                 const int step = steps - 1 - i;
-                if (!cluster_maps_wait(sh.peers, step)) u = __uint_as_float(0x7fc00000u);
+                if (!cluster_maps_wait(peers, step)) lane_set(u, __uint_as_float(0x7fc00000u));
                 for (int r = ranks - 1; r >= 0; --r) {
                     if (r == rank) last = u;
-                    const float2 t = sh.peers.map[step & 1][r][lane];
-                    u = fmaf(t.x, u, t.y);
+                    const auto m = peers.map(step, r);
+                    u = lane_fma(m.a, u, m.b);
                 }
             }
+            L mine = last;
 #pragma unroll
-            for (int v = kScanWarps - 1; v >= 0; --v) {
+            for (int v = kWarps - 1; v >= 0; --v) {
                 if (v == warp) mine = last;
-                last = fmaf(WA[v], last, WU[v]);
+                if (ranks == 1 || v > 0) last = lane_fma(sh.warp_map[p][v][0][lane], last, sh.warp_map[p][v][2][lane]);
             }
             if (ranks == 1) u = last;
 #pragma unroll
             for (int v = kWarpGroups - 1; v >= 0; --v) {
-                sh.map[warp * kWarpGroups + v][2][lane] = mine;
-                mine = fmaf(A[v], mine, U[v]);
+                entry(v, 2) = mine;
+                mine = lane_fma(A[v], mine, U[v]);
             }
         }
         __syncwarp();
-        F2 h[kScanPairs], e[kScanPairs];
-        unpack4(*reinterpret_cast<const float4 *>(&sh.map[group][1][col]), h);
-        unpack4(*reinterpret_cast<const float4 *>(&sh.map[group][2][col]), e);
+        Pairs<V> h = load_pairs<V>(&sh.map[group][1][col]), e = load_pairs<V>(&sh.map[group][2][col]);
 #pragma unroll
-        for (int j = 0; j < kScanTpt; ++j)
+        for (int j = 0; j < kTpt; ++j)
 #pragma unroll
-            for (int c = 0; c < kScanPairs; ++c) {
+            for (int c = 0; c < kPairs; ++c) {
                 const F2 before = h[c];
                 h[c] = fma2(a[j][c], h[c], b[j][c]);
                 b[j][c] = before;  // h_{t-1}
@@ -237,15 +234,14 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
         XT *dxp = dx + at;
         GT *dgp = dg + at;
 #pragma unroll
-        for (int j = kScanTpt - 1; j >= 0; --j) {
+        for (int j = kTpt - 1; j >= 0; --j) {
             if (j >= left) continue;  // past the end: the identity map, e passes through
-            const int s = s0 + j * kScanThreads;
-            F2 xv[kScanPairs], zv[kScanPairs], dv[kScanPairs], ox[kScanPairs], og[kScanPairs];
-            if (kWrite != KDA_WRITE_PLAIN) unpack4(xs[s], xv);
-            if (kGate == KDA_GATE_BOUNDED) unpack4(gs[s], zv);
-            unpack4(ds[s], dv);
+            Pairs<V> xv, zv, ox, og;
+            if (kWrite != KDA_WRITE_PLAIN) xv = XS::get(xs, st, j);
+            if (kGate == KDA_GATE_BOUNDED) zv = GS::get(gs, st, j);
+            const Pairs<V> dv = XS::get(ds, st, j);
 #pragma unroll
-            for (int c = 0; c < kScanPairs; ++c) {
+            for (int c = 0; c < kPairs; ++c) {
                 const F2 aj = a[j][c], cj = c1[kKeepC ? j : 0][c];
                 const F2 et = add2(dv[c], e[c]);
                 F2 d = b[j][c];
@@ -269,38 +265,20 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                     og[c] = mul2(og[c], mul2(mul2(f2(lower), s1), sc));
                 }
             }
-            *reinterpret_cast<XP *>(dxp + (size_t)j * D) = pack4<XT>(ox);
-            *reinterpret_cast<GP *>(dgp + (size_t)j * D) = pack4<GT>(og);
+            store_pairs<V>(dxp + (size_t)j * D, ox);
+            store_pairs<V>(dgp + (size_t)j * D, og);
         }
     }
     async_wait<0>();
-    if (dinit && warp == 0 && rank == 0 && lane_ch) dinit[(size_t)n * D + ch0 + lane] = u;
+    if (dinit && warp == 0 && rank == 0 && lane_ch) *reinterpret_cast<L *>(dinit + state_at) = u;
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_bwd(const ScanArgs &s, cudaStream_t stream) {
-    using S = BwdShape<XT, GT>;
-    auto kernel = scan_bwd<XT, GT, kGate, kWrite>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
-    if (err != cudaSuccess) return err;
-    const int blocks = (s.D + kScanCh - 1) / kScanCh;
-    const long long units = (long long)s.num_seqs * blocks;
-    const int ranks = scan_ranks(units, s.cu ? s.tokens : s.T_fixed, 152 * S::per_sm);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * ranks));
-    cfg.blockDim = dim3(kScanThreads);
-    cfg.dynamicSmemBytes = S::smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const XT *>(s.dout), s.dfinal,
-                              static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), (const float *)s.carries,
-                              s.cu, static_cast<XT *>(s.dx), static_cast<GT *>(s.dg), s.dinit, s.T_fixed,
-                              s.tokens, s.D, blocks, ranks, s.gate.lower);
+    return launch_scan<BwdShape<XT, GT>, scan_bwd<XT, GT, kGate, kWrite>>(
+        s, stream, static_cast<const XT *>(s.dout), s.dfinal, static_cast<const XT *>(s.x),
+        static_cast<const GT *>(s.g), (const float *)s.carries, s.cu, static_cast<XT *>(s.dx), static_cast<GT *>(s.dg),
+        s.dinit, s.T_fixed, s.tokens, s.D);
 }
 
 }  // namespace

@@ -157,6 +157,13 @@ def chunk_fwd(q, k, v, g, beta, scale, init_state=None, cu_seqlens=None, *, out=
     return out, final_state
 
 
+# The raw handle of a device's current stream (torch.cuda.current_stream builds an
+# object around it, 2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_HERE = contextlib.nullcontext()
+
+
 def _scope(device, stream):
     """Context in which allocations and launches of a call on ``device``'s
     tensors belong to its stream (the device's current one when None)."""
@@ -165,13 +172,14 @@ def _scope(device, stream):
             raise ValueError("stream must belong to the tensors' device")
         return torch.cuda.stream(stream)
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
 def _same_device(first, **others):
+    index = first.get_device()
     for name, t in others.items():
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError("%s must be on the same device as the other tensors" % name)
 
 
@@ -240,7 +248,7 @@ def _decode_step_slots(q, k, v, g, beta, scale, state, slots, out, stream, opts,
             _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state), _ptr(slots),
             _ptr(out), N, state.shape[0], H, dk, dv, _DTYPES[q.dtype],
             None if opts is None else ctypes.byref(opts),
-            torch.cuda.current_stream(q.device).cuda_stream))
+            _raw_stream(q.get_device())))
     return out
 
 

@@ -4,7 +4,7 @@ gated_scan_step take it with ``slots``, or [L, P, ...] over L layers."""
 import torch
 
 from . import _lib
-from .kda import _need, _ptr, _same_device, _scope
+from .kda import _need, _ptr, _raw_stream, _same_device, _scope
 
 
 def _pool(t, name, slot_dim):
@@ -52,7 +52,7 @@ def state_copy(pool, src, dst, *, source=None, slot_dim=0, stream=None):
     with _scope(pool.device, stream):
         _lib.check("kda_state_copy", _lib.lib().kda_state_copy(
             _ptr(source), source_slots, _ptr(pool), slots, _ptr(src), _ptr(dst), src.shape[0],
-            layers, nbytes, torch.cuda.current_stream(pool.device).cuda_stream))
+            layers, nbytes, _raw_stream(pool.get_device())))
     return pool
 
 
@@ -84,5 +84,5 @@ def state_compact(pool, live, *, slot_dim=0, new_slot=None, count=None, stream=N
         _lib.check("kda_state_compact", _lib.lib().kda_state_compact(
             _ptr(pool), slots, _ptr(live), _ptr(new_slot), _ptr(count), layers, nbytes,
             _ptr(workspace), workspace.numel(),
-            torch.cuda.current_stream(pool.device).cuda_stream))
+            _raw_stream(pool.get_device())))
     return new_slot, count

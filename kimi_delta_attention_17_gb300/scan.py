@@ -2,36 +2,45 @@
 + w_t x_t per channel, over whole sequences with its gradient, and one token at
 a time. Only arguments are marshalled here."""
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
-from .kda import _DTYPES, _need, _ptr, _same_device, _scope
+from .kda import _DTYPES, _need, _ptr, _raw_stream, _same_device, _scope
 
 
+@functools.lru_cache(maxsize=64)
 def _scan_options(gate, gate_lower, write):
+    """kda_scan_options by reference, one for each combination in use."""
     if gate not in _lib.GATE or write not in _lib.WRITE:
         raise ValueError("gate must be one of %s and write one of %s"
                          % (sorted(_lib.GATE), sorted(_lib.WRITE)))
-    return _lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write])
+    return ctypes.byref(_lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write]))
+
+
+def _rows(x, g, lead):
+    """Checks x and g, with ``lead`` dimensions before the channels'; returns the
+    first of them and the number of channels."""
+    _need(x, "x")
+    _need(g, "g")
+    if x.dtype not in _DTYPES or g.dtype not in _DTYPES:
+        raise ValueError("x and g must be bfloat16 or float32")
+    shape = x.shape
+    if len(shape) <= lead:
+        raise ValueError("x must be [%schannels...]" % ("B, T, " if lead == 2 else "N, "))
+    if g.shape != shape:
+        raise ValueError("g must have x's shape")
+    D = 1
+    for n in shape[lead:]:
+        D *= n
+    return shape[0], D
 
 
 def _tokens(x, g, cu_seqlens):
     """Checks x [B, T, ...], g and cu_seqlens; returns B, T, D, num_seqs."""
-    _need(x, "x")
-    if x.dim() < 3:
-        raise ValueError("x must be [B, T, channels...]")
-    if x.dtype not in _DTYPES:
-        raise ValueError("x must be bfloat16 or float32")
-    _need(g, "g")
-    if g.dtype not in _DTYPES:
-        raise ValueError("g must be bfloat16 or float32")
-    if g.shape != x.shape:
-        raise ValueError("g must have x's shape")
-    B, T = x.shape[:2]
-    D = 1
-    for n in x.shape[2:]:
-        D *= n
+    B, D = _rows(x, g, 2)
+    T = x.shape[1]
     if cu_seqlens is None:
         return B, T, D, B
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
@@ -69,14 +78,14 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
     the channels in any number of dimensions, e.g. [B, T, H, d]); g of x's shape
     (fp32, or bf16 with bf16 x); init_state [N, channels...] fp32 or None;
     cu_seqlens int32 [N + 1] (device) or None (then N = B). The number of
-    channels must be a multiple of 4.
+    channels must be a multiple of 8 (of 4 with fp32 x).
     Returns (out, final_state or None, carries or None): out the states h_t in
     x's type, final_state [N, channels...] fp32.
     ``gate``: "log" (g is log a), "logsigmoid" (a = sigmoid(g)) or "bounded"
     (log a = gate_lower * sigmoid(g)). ``write``: "plain" (w = 1), "complement"
     (w = 1 - a) or "norm" (w = sqrt(1 - a^2)).
     ``save_carries`` (or a ``carries`` buffer) keeps what gated_scan_bwd needs:
-    the fp32 state entering every 128th token, [B T // 128 + N, D].
+    the fp32 state entering every 64th token, [B T // 64 + N, D].
     Rows of ``out`` outside every sequence are left as they were."""
     B, T, D, N = _tokens(x, g, cu_seqlens)
     opts = _scan_options(gate, gate_lower, write)
@@ -99,8 +108,8 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
             carries = torch.empty((rows, D), dtype=torch.float32, device=x.device)
         _lib.check("kda_gated_scan_fwd", _lib.lib().kda_gated_scan_fwd(
             _ptr(x), _ptr(g), _ptr(init_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
-            _ptr(carries), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype], ctypes.byref(opts),
-            torch.cuda.current_stream(x.device).cuda_stream))
+            _ptr(carries), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype], opts,
+            _raw_stream(x.get_device())))
     return out, final_state, carries
 
 
@@ -135,7 +144,7 @@ def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, d
         _lib.check("kda_gated_scan_bwd", _lib.lib().kda_gated_scan_bwd(
             _ptr(dout), _ptr(dfinal_state), _ptr(x), _ptr(g), _ptr(carries), _ptr(cu_seqlens),
             _ptr(dx), _ptr(dg), _ptr(dinit_state), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype],
-            ctypes.byref(opts), torch.cuda.current_stream(x.device).cuda_stream))
+            opts, _raw_stream(x.get_device())))
     return dx, dg, dinit_state
 
 
@@ -147,14 +156,9 @@ def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log
     slot slots[n] is row n's state. Rows whose slot lies outside [0, P) (-1:
     padding) touch no state and get zeros; slots in range must be distinct.
     Returns out [N, channels...] in x's type. Options as in gated_scan_fwd."""
-    _need(x, "x")
-    if x.dim() < 2:
-        raise ValueError("x must be [N, channels...]")
-    _need(g, "g")
-    _, _, D, _ = _tokens(x.unsqueeze(0), g.unsqueeze(0), None)
+    N, D = _rows(x, g, 1)
     opts = _scan_options(gate, gate_lower, write)
     _need(state, "state", torch.float32)
-    N = x.shape[0]
     if state.shape[1:] != x.shape[1:] or state.dim() != x.dim():
         raise ValueError("state must be [slots, %s]" % ", ".join(map(str, x.shape[1:])))
     if slots is None:
@@ -171,6 +175,6 @@ def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log
             out = torch.empty_like(x)
         _lib.check("kda_gated_scan_step", _lib.lib().kda_gated_scan_step(
             _ptr(x), _ptr(g), _ptr(state), _ptr(slots), _ptr(out), N, state.shape[0], D,
-            _DTYPES[x.dtype], _DTYPES[g.dtype], ctypes.byref(opts),
-            torch.cuda.current_stream(x.device).cuda_stream))
+            _DTYPES[x.dtype], _DTYPES[g.dtype], opts,
+            _raw_stream(x.get_device())))
     return out

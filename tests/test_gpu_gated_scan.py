@@ -77,16 +77,21 @@ def check(v, gate, write, lower=-5.0, cu=None, backward=True, **kw):
 @pytest.mark.parametrize("write", ["plain", "complement", "norm"])
 @pytest.mark.parametrize("gate", ["log", "logsigmoid", "bounded"])
 def test_every_form(gate, write, types):
-    check(make(2, 301, 36, types, gate), gate, write)
+    check(make(2, 301, 72, types, gate), gate, write)
 
 
-@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8, 9, 31, 33, 127, 128, 129, 255, 256, 257, 513, 1023, 2049, 5000])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8, 9, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 513, 1023, 2049, 5000])
 @pytest.mark.parametrize("types", list(TYPES))
 def test_lengths(T, types):
     check(make(1, T, 8, types, "logsigmoid", seed=T), "logsigmoid", "complement")
 
 
-@pytest.mark.parametrize("B,T,D", [(1, 300, 4), (3, 70, 12), (1, 130, 1028), (2, 40, 4096), (64, 3, 64), (400, 1, 260),
+@pytest.mark.parametrize("T,D", [(200, 4), (77, 12), (300, 132)])
+def test_fp32_shapes(T, D):
+    check(make(2, T, D, "f32", "logsigmoid", seed=D), "logsigmoid", "norm")
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 300, 8), (3, 70, 24), (1, 130, 1032), (2, 40, 4096), (64, 3, 64), (400, 1, 264),
                                    (5, 200, 2048)])
 def test_shapes(B, T, D):
     check(make(B, T, D, "bf16", "bounded", seed=B + T + D), "bounded", "norm")
@@ -96,7 +101,7 @@ def test_shapes(B, T, D):
 @pytest.mark.parametrize("cu", [[0, 1], [0, 0, 5, 5, 133, 134, 134], [0, 128, 256, 400], [0, 700, 701, 1400],
                                 [0, 3, 6, 9, 12, 15, 18, 21], [0, 0, 0]])
 def test_packed(cu, types):
-    v = make(1, max(cu[-1], 0), 20, types, "log", seed=len(cu), N=len(cu) - 1)
+    v = make(1, max(cu[-1], 0), 24, types, "log", seed=len(cu), N=len(cu) - 1)
     check(v, "log", "complement", cu=cu)
 
 
@@ -111,11 +116,11 @@ def test_many_packed_sequences():
 
 
 def test_rows_outside_every_sequence_stay():
-    v = make(1, 300, 12, "bf16", N=2)
+    v = make(1, 300, 16, "bf16", N=2)
     c = cuda(v)
     cu = torch.tensor([7, 150, 260], dtype=torch.int32, device="cuda")
     out = torch.full_like(c["x"], 3.0)
-    carries = torch.full((300 // 128 + 2, 12), 5.0, device="cuda")
+    carries = torch.full((300 // 64 + 2, 16), 5.0, device="cuda")
     gated_scan_fwd(c["x"], c["g"], c["init"], cu, out=out, carries=carries)
     dx, dg = torch.full_like(c["x"], 4.0), torch.full_like(c["g"], 6.0)
     gated_scan_bwd(c["dout"], c["x"], c["g"], carries, cu, dfinal_state=c["dfinal"], dx=dx, dg=dg)
@@ -264,7 +269,7 @@ def test_offsets_past_32_bits():
 @pytest.mark.parametrize("gate", ["log", "logsigmoid", "bounded"])
 def test_step(gate, write, types):
     """A pool: rows in any order, padding and slots out of range; the rest of the pool stays."""
-    D, P = 36, 9
+    D, P = 40, 9
     v = make(1, 6, D, types, gate)
     pool0 = torch.randn(P, D, generator=torch.Generator().manual_seed(4))
     slots = [4, -1, 0, P, 8, 2]
@@ -284,7 +289,7 @@ def test_step(gate, write, types):
     assert torch.equal(pool.cpu(), want)
 
 
-@pytest.mark.parametrize("N,D", [(1, 4), (1, 2560), (3, 512), (300, 1028)])
+@pytest.mark.parametrize("N,D", [(1, 8), (1, 2560), (3, 512), (300, 1032)])
 def test_step_dense(N, D):
     v = make(1, N, D, "bf16", "logsigmoid")
     state0 = torch.randn(N, D, generator=torch.Generator().manual_seed(4))
@@ -357,7 +362,7 @@ def test_refusals():
         gated_scan_fwd(x, g.bfloat16())
     with pytest.raises(RuntimeError, match="INVALID"):
         gated_scan_fwd(x, g, gate="bounded", gate_lower=1.0)
-    carries = torch.zeros(2, 8, device="cuda")
+    carries = torch.zeros(2, 8, device="cuda")  # 2 x 8 tokens: 16 // 64 + 2 rows
     for bad in (dict(dout=x.bfloat16()), dict(dout=None), dict(carries=carries[:1]), dict(carries=None),
                 dict(dx=x[:1]), dict(dg=g.bfloat16()), dict(dfinal_state=carries[0]), dict(dinit_state=x)):
         with pytest.raises((ValueError, TypeError)):

@@ -54,6 +54,7 @@ def test_scan_refusals(L, call, tensors):
     assert call(L, o=opts(gate=2, lower=-5.0, write=2)) == UNSUPPORTED
     assert call(L, cu=FAKE, N=5) == UNSUPPORTED
     assert call(L, D=8, dt=0, gdt=1) == UNSUPPORTED     # fp32 inputs with bf16 gates
+    assert call(L, D=12) == UNSUPPORTED                 # bf16 rows of 24 bytes
 
 
 def test_scan_optional_pointers(L):
@@ -64,8 +65,8 @@ def test_scan_optional_pointers(L):
 
 def test_carries_size(L):
     f = L.kda_gated_scan_carries_size
-    assert f(1, 127, 8, 1) == 32 and f(1, 128, 8, 1) == 64 and f(2, 128, 8, 2) == 128
-    assert f(1, 1000, 8, 9) == (1000 // 128 + 9) * 32
+    assert f(1, 63, 8, 1) == 32 and f(1, 64, 8, 1) == 64 and f(2, 64, 8, 2) == 128
+    assert f(1, 1000, 8, 9) == (1000 // 64 + 9) * 32
     assert f(1, 0, 8, 3) == 96
     for bad in ((0, 1, 8, 1), (1, -1, 8, 1), (1, 1, 0, 1), (1, 1, 8, 0), (2, 1, 8, 3)):
         assert f(*bad) == 0
