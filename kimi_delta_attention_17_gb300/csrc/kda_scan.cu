@@ -33,6 +33,7 @@ struct FwdShape {
     struct Shared {
         float map[Tiling::groups][2][ch];  // (A, H) of each group's tokens; then H gives way to the state entering them
         L warp_map[2][warps][2][32];  // (A, H) of each warp's tokens
+        int sequence;
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(FwdShape<XT, GT>::threads, FwdShape<XT, GT>::p
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
-         float lower) {
+         int ordered, float lower) {
     using S = FwdShape<XT, GT>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -61,7 +62,8 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
-    const int n = (int)(unit / (unsigned)blocks);
+    int n = (int)(unit / (unsigned)blocks);
+    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh.map[0][0][0]), &sh.sequence);
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));  // this thread's channels, and a lane's where warps compose
     const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;

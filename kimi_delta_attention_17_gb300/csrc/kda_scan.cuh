@@ -431,6 +431,27 @@ __device__ __forceinline__ void scan_bounds(const int32_t *cu, int n, int T_fixe
     end = min(max((long long)cu[n + 1], begin), tokens);
 }
 
+// Packed sequences are taken longest first (ties by index): the sequence whose
+// place in that order is k. All threads; up to kScanThreads sequences.
+__device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int k, long long tokens, int *lens,
+                                           int *found) {
+    const int tid = threadIdx.x;
+    if (tid < num_seqs) {
+        long long begin, end;
+        scan_bounds(cu, tid, 0, tokens, begin, end);
+        lens[tid] = (int)(end - begin);
+    }
+    __syncthreads();
+    if (tid < num_seqs) {
+        const int mine = lens[tid];
+        int before = 0;
+        for (int m = 0; m < num_seqs; ++m) before += lens[m] > mine || (lens[m] == mine && m < tid);
+        if (before == k) *found = tid;
+    }
+    __syncthreads();
+    return *found;
+}
+
 // Row of `carries` that holds the state entering token
 // KDA_SCAN_CARRY_TOKENS * i of the sequence.
 __device__ __forceinline__ long long carry_row(long long begin, int n, long long i) {
@@ -478,7 +499,11 @@ struct ScanFits {
 // 420 us with 1, 123 with 4, 88 with 8, the most that fit, 126 with 9). Where
 // not even two do, up to 4 as long as that makes no more than five rounds of
 // CTAs: several rounds of short ones leave the SMs less unevenly loaded than
-// one of long ones (512 pairs of 4096 tokens: 230 us with 2, 193 with 4).
+// one of long ones (512 pairs of 4096 tokens: 230 us with 2, 193 with 4). For
+// packed sequences, whose lengths the host does not know, up to 8 within three
+// and a half rounds, the longest sequences first (24 of 65536 tokens in all,
+// 2048 channels, backward: 314 us with 1, 246 with 2, 269 with 4; forward 202
+// with 1, 145 with 2, 149 with 3, 171 with 6).
 template <typename S, auto kKernel, typename... A>
 cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     static ScanFits fits;  // one for each kernel
@@ -519,17 +544,22 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
         if (e == cudaSuccess) fits.clusters[dev][ranks].store(n, std::memory_order_relaxed);
         return n;
     };
-    const long long longest = s.cu ? s.tokens : s.T_fixed;
+    const long long mean = s.tokens / s.num_seqs;
     int ranks = kScanMaxRanks;
-    while (ranks > 1 && ((long long)(ranks - 1) * S::tile >= longest || fit(ranks) < units)) --ranks;
-    if (ranks == 1 && units > fit(2)) {
-        const long long mean = s.tokens / s.num_seqs;
-        ranks = 4;
-        while (ranks > 1 && (ranks * units > 5LL * fit(1) || ranks * S::tile > mean)) ranks /= 2;
+    if (s.cu && s.num_seqs > 1) {
+        ranks = 8;
+        while (ranks > 1 && (2 * ranks * units > 7LL * fit(1) || ranks * S::tile > 2 * mean)) --ranks;
+    } else {
+        while (ranks > 1 && ((long long)(ranks - 1) * S::tile >= mean || fit(ranks) < units)) --ranks;
+        if (ranks == 1 && units > fit(2)) {
+            ranks = 4;
+            while (ranks > 1 && (ranks * units > 5LL * fit(1) || ranks * S::tile > mean)) ranks /= 2;
+        }
     }
+    const int ordered = s.cu && s.num_seqs <= kScanThreads ? s.num_seqs : 0;
     if (err != cudaSuccess) return err;
     shape(ranks);
-    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, s.gate.lower);
+    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, ordered, s.gate.lower);
 }
 
 // fn<storage type, gate type, gate, write>(args, stream) for a checked call.

@@ -27,6 +27,7 @@ struct BwdShape {
     struct Shared {
         float map[Tiling::groups][3][ch];     // A, H, U of each group's tokens; then the state and the gradient entering them
         L warp_map[2][warps][3][32];  // A, H, U of each warp's tokens
+        int sequence;
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (2 * XS::bytes_per_stage + GS::bytes_per_stage);
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(BwdShape<XT, GT>::threads, BwdShape<XT, GT>::p
 scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict__ x,
          const GT *__restrict__ g, const float *__restrict__ carries, const int32_t *__restrict__ cu,
          XT *__restrict__ dx, GT *__restrict__ dg, float *dinit, int T_fixed, long long tokens, int D,
-         int blocks, int ranks, float lower) {
+         int blocks, int ranks, int ordered, float lower) {
     using S = BwdShape<XT, GT>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -56,7 +57,8 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;
-    const int n = (int)(unit / (unsigned)blocks);
+    int n = (int)(unit / (unsigned)blocks);
+    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh.map[0][0][0]), &sh.sequence);
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));
     const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
