@@ -33,7 +33,6 @@ struct FwdShape {
     struct Shared {
         float map[Tiling::groups][2][ch];  // (A, H) of each group's tokens; then H gives way to the state entering them
         L warp_map[2][warps][2][32];  // (A, H) of each warp's tokens
-        int sequence;
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
@@ -58,12 +57,12 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     void *xs = smem_raw + S::stages * GS::bytes_per_stage;
     __shared__ __align__(16) typename S::Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid / kScanLanes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
     int n = (int)(unit / (unsigned)blocks);
-    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh.map[0][0][0]), &sh.sequence);
+    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh));
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));  // this thread's channels, and a lane's where warps compose
     const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
@@ -78,7 +77,8 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
-    const int len = (int)(end - begin);
+    begin = uniform(begin);
+    const int len = uniform((int)(end - begin));
     const int super = kTile * ranks;  // tokens per cluster step
     const int steps = (int)(((long long)len + super - 1) / super);
 

@@ -418,6 +418,14 @@ __device__ __forceinline__ bool cluster_maps_wait(const ClusterMaps<kCh> &m, int
     return false;
 }
 
+// A value that is the same in every lane, so that the compiler knows: it then
+// keeps the loops and branches that depend on it in uniform registers (an
+// unmarked sequence number cost both scans 10 %).
+template <typename T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // Tokens [begin, end) of sequence n among `tokens`: offsets are clamped, so
 // that no content of cu_seqlens leads out of the arrays.
 __device__ __forceinline__ void scan_bounds(const int32_t *cu, int n, int T_fixed, long long tokens,
@@ -433,8 +441,7 @@ __device__ __forceinline__ void scan_bounds(const int32_t *cu, int n, int T_fixe
 
 // Packed sequences are taken longest first (ties by index): the sequence whose
 // place in that order is k. All threads; up to kScanThreads sequences.
-__device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int k, long long tokens, int *lens,
-                                           int *found) {
+__device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int k, long long tokens, int *lens) {
     const int tid = threadIdx.x;
     if (tid < num_seqs) {
         long long begin, end;
@@ -446,10 +453,12 @@ __device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int 
         const int mine = lens[tid];
         int before = 0;
         for (int m = 0; m < num_seqs; ++m) before += lens[m] > mine || (lens[m] == mine && m < tid);
-        if (before == k) *found = tid;
+        if (before == k) lens[kScanThreads] = tid;
     }
     __syncthreads();
-    return *found;
+    const int n = uniform(lens[kScanThreads]);
+    __syncthreads();
+    return n;
 }
 
 // Row of `carries` that holds the state entering token

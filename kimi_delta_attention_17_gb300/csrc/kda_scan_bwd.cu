@@ -27,7 +27,6 @@ struct BwdShape {
     struct Shared {
         float map[Tiling::groups][3][ch];     // A, H, U of each group's tokens; then the state and the gradient entering them
         L warp_map[2][warps][3][32];  // A, H, U of each warp's tokens
-        int sequence;
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (2 * XS::bytes_per_stage + GS::bytes_per_stage);
@@ -53,12 +52,12 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     void *ds = smem_raw + S::stages * (GS::bytes_per_stage + XS::bytes_per_stage);
     __shared__ __align__(16) typename S::Shared sh;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = tid / kScanLanes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
     const int rank = ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;
     int n = (int)(unit / (unsigned)blocks);
-    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh.map[0][0][0]), &sh.sequence);
+    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh));
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));
     const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
@@ -74,7 +73,8 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
-    const int len = (int)(end - begin);
+    begin = uniform(begin);
+    const int len = uniform((int)(end - begin));
     const int super = kTile * ranks;
     const int steps = (int)(((long long)len + super - 1) / super);
 
