@@ -578,15 +578,18 @@ kda_status kda_gated_scan_step(const void *x, const void *g, float *state, const
  *             outside [0, num_slots) (-1 by custom), or whose src is not below
  *             the source's slots, are skipped.
  *  n          0 .. KDA_STATE_COPY_MAX, else KDA_ERR_UNSUPPORTED
- *  layers     >= 1; slot_bytes a positive multiple of 16 (64 KiB per head for a
- *             128 x 128 state)
+ *  layers     >= 1; slot_bytes a positive multiple of 16, at most 2^34 (64 KiB per
+ *             head for a 128 x 128 state)
  * source and pool 16-byte aligned. No workspace; one launch.
  */
 kda_status kda_state_copy(const void *source, int source_slots, void *pool, int num_slots,
                           const int32_t *src, const int32_t *dst, int n, int layers,
                           size_t slot_bytes, cudaStream_t stream);
 
-/* Bytes of device workspace kda_state_compact needs (0 for num_slots <= 0). */
+/*
+ * Bytes of device workspace kda_state_compact needs: 0 for up to 4096 slots
+ * (and for num_slots <= 0).
+ */
 size_t kda_state_compact_workspace_size(int num_slots);
 
 /*
@@ -601,7 +604,7 @@ size_t kda_state_compact_workspace_size(int num_slots);
  *             for a slot that was not live
  *  count      int32 [1] (written): n
  *  workspace  kda_state_compact_workspace_size(num_slots) bytes, 256-byte
- *             aligned; contents on entry are ignored
+ *             aligned (NULL where that is 0); contents on entry are ignored
  * pool 16-byte aligned, new_slot and count 4-byte; layers and slot_bytes as
  * kda_state_copy.
  */

@@ -541,10 +541,10 @@ extern "C" kda_status kda_gated_scan_step(const void *x, const void *g, float *s
 namespace {
 
 // A pool's sizes: whole 16-byte pieces, and a size that byte offsets can hold.
-constexpr size_t kPoolMost = (size_t)1 << 46;
+constexpr size_t kPoolMost = (size_t)1 << 46, kSlotMost = (size_t)1 << 34;
 bool pool_ok(int num_slots, int layers, size_t slot_bytes) {
     if (num_slots <= 0 || layers <= 0 || slot_bytes == 0 || slot_bytes % 16 != 0) return false;
-    return slot_bytes <= kPoolMost && (size_t)num_slots * (size_t)layers <= kPoolMost / slot_bytes;
+    return slot_bytes <= kSlotMost && (size_t)num_slots * (size_t)layers <= kPoolMost / slot_bytes;
 }
 
 }  // namespace
@@ -580,7 +580,8 @@ extern "C" kda_status kda_state_compact(void *pool, int num_slots, const uint8_t
     if (!pool_ok(num_slots, layers, slot_bytes)) return KDA_ERR_INVALID_ARGUMENT;
     if (!pool || !live || !new_slot || !count) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16(pool) || !aligned4(new_slot) || !aligned4(count)) return KDA_ERR_INVALID_ARGUMENT;
-    if (!workspace || workspace_bytes < compact_workspace(num_slots)) return KDA_ERR_WORKSPACE;
+    const size_t need = compact_workspace(num_slots);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
     const cudaError_t err = launch_state_compact(pool, num_slots, live, new_slot, count, layers, slot_bytes,
                                                  workspace, stream);

@@ -31,10 +31,13 @@ constexpr int copy_hash_size(int n) {
     return h;
 }
 
+// `kItems` 16-byte pieces a thread in each column buffer. Sizes in pieces.
+template <int kItems>
 __global__ void __launch_bounds__(kPoolThreads)
-state_copy_kernel(const char *source, long long source_slots, char *pool, long long num_slots,
+state_copy_kernel(const uint4 *source, int source_slots, uint4 *pool, int num_slots,
                   const int32_t *__restrict__ src, const int32_t *__restrict__ dst, int n, int hash_size,
-                  int layers, long long slot_bytes, int buffer_bytes, int list_bytes) {
+                  int layers, uint32_t slot, int list_bytes) {
+    constexpr int kBuffer = kItems * kPoolThreads;
     extern __shared__ __align__(128) unsigned char smem[];
     int2 *list = reinterpret_cast<int2 *>(smem);  // (source or -1, destination): copies from the front,
                                                   // zeroed slots from the back
@@ -76,22 +79,32 @@ state_copy_kernel(const char *source, long long source_slots, char *pool, long l
     if (copies + zeros == 0) return;
     // Width of a column: as wide as a buffer allows, but narrow enough that
     // there are two columns for every CTA.
-    int shift = 10;  // 16-byte pieces per column and entry, as a power of two
-    while (shift > 0 && ((long long)copies << (shift + 4)) > buffer_bytes) --shift;
-    while (shift > 3 && layers * ((slot_bytes + (16LL << shift) - 1) >> (shift + 4)) < 2LL * gridDim.x) --shift;
-    const long long columns = (slot_bytes + (16LL << shift) - 1) >> (shift + 4);
-    const long long units = columns * layers;
-    const int pieces = copies << shift, mask = (1 << shift) - 1;
+    int shift = 10;  // pieces per column and entry, as a power of two
+    while (shift > 0 && ((long long)copies << shift) > kBuffer) --shift;
+    while (shift > 3 && layers * (((long long)slot + (1 << shift) - 1) >> shift) < 2LL * gridDim.x) --shift;
+    const uint32_t columns = (slot + (1u << shift) - 1) >> shift;
+    const long long units = (long long)columns * layers;
+    const uint32_t mask = (1u << shift) - 1;
 
+    // Which pieces a thread takes is the same in every column; what is left of
+    // an item there is two 32-bit products, a copy in and a copy out.
+    uint4 *buf4 = reinterpret_cast<uint4 *>(buf) + tid;
+    int2 entry[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int p = tid + k * kPoolThreads;
+        entry[k] = p < copies << shift ? list[p >> shift] : make_int2(-1, -1);
+    }
+    const uint32_t in = (uint32_t)tid & mask;  // kPoolThreads is a multiple of a column's pieces, or
+                                               // a column's pieces of kPoolThreads
+    auto inside = [&](int k) { return shift > 8 ? ((uint32_t)(tid + k * kPoolThreads) & mask) : in; };
     auto gather = [&](long long unit, int b) {
-        const long long layer = unit / columns, off = (unit % columns) << (shift + 4);
-        const char *from = source + layer * source_slots * slot_bytes + off;
-        for (int p = tid; p < pieces; p += kPoolThreads) {
-            const long long in = (long long)(p & mask) * 16;
-            if (off + in < slot_bytes)
-                async16(buf + (size_t)b * buffer_bytes + (size_t)p * 16,
-                        from + (long long)list[p >> shift].x * slot_bytes + in);
-        }
+        const uint32_t off = (uint32_t)(unit % columns) << shift;
+        const uint4 *from = source + (size_t)(unit / columns) * source_slots * slot + off;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k)
+            if (entry[k].x >= 0 && off + inside(k) < slot)
+                async16(buf4 + (size_t)(b * kItems + k) * kPoolThreads, from + (size_t)(uint32_t)entry[k].x * slot + inside(k));
     };
     long long unit = blockIdx.x;
     if (unit < units) gather(unit, 0);
@@ -101,26 +114,21 @@ state_copy_kernel(const char *source, long long source_slots, char *pool, long l
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();  // every source of this column has been read
-        const long long layer = unit / columns, off = (unit % columns) << (shift + 4);
-        char *to = pool + layer * num_slots * slot_bytes + off;
-        for (int p = tid; p < pieces; p += kPoolThreads) {  // the pieces this thread gathered
-            const long long in = (long long)(p & mask) * 16;
-            if (off + in < slot_bytes)
-                *reinterpret_cast<uint4 *>(to + (long long)list[p >> shift].y * slot_bytes + in) =
-                    *reinterpret_cast<const uint4 *>(buf + (size_t)b * buffer_bytes + (size_t)p * 16);
-        }
-        for (int p = tid; p < zeros << shift; p += kPoolThreads) {
-            const long long in = (long long)(p & mask) * 16;
-            if (off + in < slot_bytes)
-                *reinterpret_cast<uint4 *>(to + (long long)list[n - 1 - (p >> shift)].y * slot_bytes + in) =
-                    make_uint4(0, 0, 0, 0);
-        }
+        const uint32_t off = (uint32_t)(unit % columns) << shift;
+        uint4 *to = pool + (size_t)(unit / columns) * num_slots * slot + off;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k)  // the pieces this thread gathered
+            if (entry[k].x >= 0 && off + inside(k) < slot)
+                to[(size_t)(uint32_t)entry[k].y * slot + inside(k)] = buf4[(size_t)(b * kItems + k) * kPoolThreads];
+        for (int p = tid; p < zeros << shift; p += kPoolThreads)
+            if (off + ((uint32_t)p & mask) < slot)
+                to[(size_t)(uint32_t)list[n - 1 - (p >> shift)].y * slot + ((uint32_t)p & mask)] = make_uint4(0, 0, 0, 0);
     }
 }
 
 // ---- compaction
 
-// One CTA: counts the live slots, then lists in order the live slots at or
+// Larger pools. One CTA: counts the live slots, then lists in order the live slots at or
 // above the count and the holes below it (as many of one as of the other).
 // Workspace: moves, then mover[num_slots], hole[num_slots].
 constexpr int kPlanThreads = 1024;
@@ -180,22 +188,20 @@ compact_plan_kernel(const uint8_t *__restrict__ live, int num_slots, int32_t *__
     }
 }
 
-// Copies mover[n - m + k] to hole[k]: sources and destinations are disjoint, so
-// any order does. A unit is 16 KiB of one slot.
+// Copies slot mover[k] to hole[k] for k < m: sources and destinations are
+// disjoint, so any order does. A unit is 16 KiB of one slot.
 constexpr int kMoveUnroll = 4;
 constexpr long long kMoveBytes = 16LL * kPoolThreads * kMoveUnroll;
 
-__global__ void __launch_bounds__(kPoolThreads)
-compact_move_kernel(char *pool, int num_slots, const int32_t *__restrict__ count,
-                    const int *__restrict__ moves, const int *__restrict__ mover,
-                    const int *__restrict__ hole, int layers, long long slot_bytes) {
-    const int m = *moves, first = *count - m;
+template <typename I>
+__device__ __forceinline__ void move_slots(char *pool, int num_slots, int m, const I *mover, const I *hole, int layers,
+                                           long long slot_bytes) {
     const long long pieces = (slot_bytes + kMoveBytes - 1) / kMoveBytes;
     const long long units = pieces * m * layers;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const long long piece = u % pieces, k = u / pieces % m, layer = u / pieces / m;
         char *base = pool + layer * num_slots * slot_bytes;
-        const char *from = base + (long long)mover[first + k] * slot_bytes;
+        const char *from = base + (long long)mover[k] * slot_bytes;
         char *to = base + (long long)hole[k] * slot_bytes;
         const long long at = piece * kMoveBytes + threadIdx.x * 16;
         uint4 v[kMoveUnroll];
@@ -210,6 +216,73 @@ compact_move_kernel(char *pool, int num_slots, const int32_t *__restrict__ count
             if (o < slot_bytes) *reinterpret_cast<uint4 *>(to + o) = v[j];
         }
     }
+}
+
+// The moves that compact_plan_kernel listed.
+__global__ void __launch_bounds__(kPoolThreads)
+compact_move_kernel(char *pool, int num_slots, const int32_t *__restrict__ count,
+                    const int *__restrict__ moves, const int *__restrict__ mover,
+                    const int *__restrict__ hole, int layers, long long slot_bytes) {
+    move_slots(pool, num_slots, *moves, mover + (*count - *moves), hole, layers, slot_bytes);
+}
+
+// Pools of up to kFusedSlots slots: one launch, in which every CTA makes the
+// lists for itself in shared memory (a plan by one CTA and a second launch cost
+// 10 us more at 512 slots).
+constexpr int kFusedSlots = 4096, kFusedPer = kFusedSlots / kPoolThreads;
+
+__global__ void __launch_bounds__(kPoolThreads)
+compact_kernel(char *pool, int num_slots, const uint8_t *__restrict__ live, int32_t *__restrict__ new_slot,
+               int32_t *__restrict__ count, int layers, long long slot_bytes) {
+    __shared__ __align__(16) uint8_t flags[kFusedSlots];
+    __shared__ uint16_t mover[kFusedSlots / 2], hole[kFusedSlots / 2];
+    __shared__ int warp_sum[kPoolThreads / 32], below;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int s = tid; s < kFusedSlots; s += kPoolThreads) flags[s] = s < num_slots && live[s] != 0;
+    if (tid == 0) below = 0;
+    __syncthreads();
+    // Each thread counts a run of slots; `before` becomes the live slots below it.
+    uint32_t mine = 0;  // bit i: slot first + i lives
+    const int first = tid * kFusedPer;
+#pragma unroll
+    for (int i = 0; i < kFusedPer; ++i) mine |= (uint32_t)flags[first + i] << i;
+    int before = __popc(mine);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += up;
+    }
+    if (lane == 31) warp_sum[warp] = before;
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kPoolThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        n += warp_sum[w];
+    }
+    before -= __popc(mine);
+    // Live slots below n: n minus the holes there.
+    const int inside = min(max(n - first, 0), kFusedPer);
+    const uint32_t low = mine & ((1u << inside) - 1);
+    const int some = __reduce_add_sync(0xffffffffu, __popc(low));
+    if (lane == 0) atomicAdd(&below, some);
+    __syncthreads();
+    const int kept = below, m = n - kept;
+    for (int i = 0; i < kFusedPer; ++i) {
+        const int s = first + i;
+        if (s >= num_slots) break;
+        const bool alive = mine >> i & 1;
+        if (!alive && s < n) hole[s - before] = (uint16_t)s;
+        if (alive && s >= n) mover[before - kept] = (uint16_t)s;
+        if (blockIdx.x == 0 && !(alive && s >= n)) new_slot[s] = alive ? s : -1;
+        before += alive;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        for (int k = tid; k < m; k += kPoolThreads) new_slot[mover[k]] = hole[k];
+        if (tid == 0) *count = n;
+    }
+    move_slots(pool, num_slots, m, mover, hole, layers, slot_bytes);
 }
 
 cudaError_t sm_count(int *n) {
@@ -227,22 +300,25 @@ cudaError_t launch_state_copy(const void *source, int source_slots, void *pool, 
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    // Two CTAs per SM; up to 4096 entries of 16 bytes need an SM's whole
-    // shared memory for one.
-    const bool wide = n > 1024;
+    // Two CTAs per SM; beyond 1024 entries a column of one piece each, and the
+    // list, need an SM's whole shared memory for one.
     const size_t lists = copy_list_bytes(n);
-    const int buffer = wide ? 90 * 1024 : 48 * 1024;
-    const size_t smem = lists + 2 * (size_t)buffer;
-    err = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    state_copy_kernel<<<sms * (wide ? 1 : 2), kPoolThreads, smem, stream>>>(
-        static_cast<const char *>(source ? source : pool), source ? source_slots : num_slots,
-        static_cast<char *>(pool), num_slots, src, dst, n, copy_hash_size(n), layers, (long long)slot_bytes,
-        buffer, (int)lists);
-    return cudaGetLastError();
+    auto launch = [&](auto kernel, int items, int per_sm) {
+        const size_t smem = lists + 2 * (size_t)items * kPoolThreads * 16;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        kernel<<<sms * per_sm, kPoolThreads, smem, stream>>>(
+            static_cast<const uint4 *>(source ? source : pool), source ? source_slots : num_slots,
+            static_cast<uint4 *>(pool), num_slots, src, dst, n, copy_hash_size(n), layers, (uint32_t)(slot_bytes / 16),
+            (int)lists);
+        return cudaGetLastError();
+    };
+    return n > 1024 ? launch(state_copy_kernel<22>, 22, 1) : launch(state_copy_kernel<12>, 12, 2);
 }
 
-size_t compact_workspace(int num_slots) { return kPlanHeader + 2 * align_up((size_t)num_slots * 4, 256); }
+size_t compact_workspace(int num_slots) {
+    return num_slots <= kFusedSlots ? 0 : kPlanHeader + 2 * align_up((size_t)num_slots * 4, 256);
+}
 
 cudaError_t launch_state_compact(void *pool, int num_slots, const uint8_t *live, int32_t *new_slot,
                                  int32_t *count, int layers, size_t slot_bytes, void *workspace,
@@ -250,6 +326,11 @@ cudaError_t launch_state_compact(void *pool, int num_slots, const uint8_t *live,
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
+    if (num_slots <= kFusedSlots) {
+        compact_kernel<<<sms * 6, kPoolThreads, 0, stream>>>(static_cast<char *>(pool), num_slots, live, new_slot,
+                                                             count, layers, (long long)slot_bytes);
+        return cudaGetLastError();
+    }
     char *ws = static_cast<char *>(workspace);
     int *moves = reinterpret_cast<int *>(ws);
     int *mover = reinterpret_cast<int *>(ws + kPlanHeader);

@@ -80,9 +80,8 @@ def state_compact(pool, live, *, slot_dim=0, new_slot=None, count=None, stream=N
         if count is None:
             count = torch.empty(1, dtype=torch.int32, device=pool.device)
         need = int(_lib.lib().kda_state_compact_workspace_size(slots))
-        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device) if need else None
         _lib.check("kda_state_compact", _lib.lib().kda_state_compact(
             _ptr(pool), slots, _ptr(live), _ptr(new_slot), _ptr(count), layers, nbytes,
-            _ptr(workspace), workspace.numel(),
-            _raw_stream(pool.get_device())))
+            _ptr(workspace), need, _raw_stream(pool.get_device())))
     return new_slot, count

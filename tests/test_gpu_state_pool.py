@@ -107,7 +107,7 @@ def compacted(pool, live):
 
 
 @pytest.mark.parametrize("P,share", [(1, 0.0), (1, 1.0), (2, 0.5), (33, 0.0), (33, 1.0), (40, 0.3), (1024, 0.6),
-                                     (1025, 0.5), (5000, 0.2)])
+                                     (1025, 0.5), (4096, 0.5), (4096, 0.9), (4097, 0.5), (5000, 0.2)])
 @pytest.mark.parametrize("L,floats", [(1, 4), (2, 516)])
 def test_compact(P, share, L, floats):
     rng = random.Random(P)

@@ -111,21 +111,23 @@ def test_pool_refusals(L):
     assert copy(source=FAKE - 3 * 2 * 64, sp=3) == UNSUPPORTED
     for bad in (dict(pool=None), dict(pool=FAKE + 8), dict(src=None), dict(dst=None), dict(src=FAKE + 2),
                 dict(dst=FAKE + 2), dict(n=-1), dict(P=0), dict(layers=0), dict(nbytes=0), dict(nbytes=24),
-                dict(nbytes=1 << 47), dict(P=2 ** 30, layers=2 ** 30), dict(source=FAKE + 8, sp=3),
+                dict(nbytes=1 << 35), dict(P=2 ** 30, layers=2 ** 30), dict(source=FAKE + 8, sp=3),
                 dict(source=far, sp=0), dict(source=FAKE, sp=4), dict(source=far - 16, sp=3),
                 dict(source=FAKE - 3 * 2 * 64 + 16, sp=3)):
         assert copy(**bad) == INVALID, bad
 
-    need = L.kda_state_compact_workspace_size(100)
-    assert need >= 2 * 4 * 100 and L.kda_state_compact_workspace_size(0) == 0
+    need = L.kda_state_compact_workspace_size(5000)
+    assert need >= 2 * 4 * 5000
+    assert [L.kda_state_compact_workspace_size(p) for p in (-1, 0, 1, 4096)] == [0, 0, 0, 0]
 
     def compact(**kw):
-        a = dict(pool=FAKE, P=100, live=FAKE, new=FAKE, count=FAKE, layers=1, nbytes=64, ws=FAKE, wsb=need - 1)
+        a = dict(pool=FAKE, P=5000, live=FAKE, new=FAKE, count=FAKE, layers=1, nbytes=64, ws=FAKE, wsb=need - 1)
         a.update(kw)
         return L.kda_state_compact(*a.values(), None)
     assert compact() == WORKSPACE
     assert compact(ws=None, wsb=need) == WORKSPACE
     assert compact(ws=FAKE + 16, wsb=need) == WORKSPACE
+    assert compact(P=100, ws=FAKE + 16, wsb=0) == WORKSPACE
     for bad in (dict(pool=None), dict(live=None), dict(new=None), dict(count=None), dict(P=0), dict(layers=-1),
                 dict(nbytes=8), dict(pool=FAKE + 4), dict(new=FAKE + 1), dict(count=FAKE + 2)):
         assert compact(**bad) == INVALID, bad
