@@ -41,12 +41,13 @@ struct FwdShape {
     static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
-template <typename XT, typename GT, int kGate, int kWrite>
+// kNarrow: a sequence for each warp (ScanOrder).
+template <typename XT, typename GT, int kGate, int kWrite, bool kNarrow>
 __global__ void __launch_bounds__(FwdShape<XT, GT>::threads, FwdShape<XT, GT>::per_sm)
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
-         int ordered, float lower) {
+         int num_seqs, int order, float lower) {
     using S = FwdShape<XT, GT>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -58,14 +59,15 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     __shared__ __align__(16) typename S::Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
-    const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+    const int rank = !kNarrow && ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
     int n = (int)(unit / (unsigned)blocks);
-    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh));
+    if (!kNarrow && order == kOrderLongest) n = kth_longest(cu, num_seqs, n, tokens, reinterpret_cast<int *>(&sh));
+    if (kNarrow) n = uniform(n * kWarps + warp);
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));  // this thread's channels, and a lane's where warps compose
-    const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
+    const bool has_ch = ch0 + col < D && n < num_seqs, lane_ch = ch0 + lane * kLaneCh < D && n < num_seqs;
 
     // In every warp, by lane: the state at the cluster's next tiles. Read before
     // the cluster's first barrier: final_state may be the same memory.
@@ -73,7 +75,7 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     lane_set(carry, 0.f);
     const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
     if (init && lane_ch) carry = *reinterpret_cast<const L *>(init + state_at);
-    if (ranks > 1) cluster_maps_init(peers);
+    if (!kNarrow && ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
@@ -84,9 +86,10 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
 
     // Of this step: tokens from this thread's first one to the sequence's end
     // (none left where negative), and the first one's element.
-    int left = has_ch ? len - (rank * kTile + group * kTpt) : -1;
+    const int first_token = rank * kTile + (kNarrow ? lane / kScanLanes : group) * kTpt;
+    int left = has_ch ? len - first_token : -1;
     const int less = has_ch ? super : 0;
-    size_t at = (size_t)(begin + (long long)rank * kTile + group * kTpt) * D + ch0 + col;
+    size_t at = (size_t)(begin + first_token) * D + ch0 + col;
     const size_t stride = (size_t)super * D;
     auto prefetch = [&](int i, int left, size_t from) {
         const int st = i % S::stages;
@@ -161,7 +164,9 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
         __syncthreads();  // warp_map's halves alternate: the only barrier of a step
         {
             L first = carry;  // the state entering the CTA's tile
-            if (ranks > 1) {
+            if (kNarrow) {
+                carry = lane_fma(sh.warp_map[i & 1][warp][0][lane], carry, sh.warp_map[i & 1][warp][1][lane]);
+            } else if (!kNarrow && ranks > 1) {
                 if (warp == 0) {
                     L TA, TH;
                     lane_set(TA, 1.f);
@@ -182,15 +187,17 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
                 }
             }
             L mine = first;  // the state entering the warp's tokens
+            if (!kNarrow) {
 #pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                if (v == warp) mine = first;
-                if (ranks == 1 || v + 1 < kWarps)
-                    first = lane_fma(sh.warp_map[i & 1][v][0][lane], first, sh.warp_map[i & 1][v][1][lane]);
+                for (int v = 0; v < kWarps; ++v) {
+                    if (v == warp) mine = first;
+                    if (ranks == 1 || v + 1 < kWarps)
+                        first = lane_fma(sh.warp_map[i & 1][v][0][lane], first, sh.warp_map[i & 1][v][1][lane]);
+                }
+                if (ranks == 1) carry = first;
             }
-            if (ranks == 1) carry = first;
             // The states that the backward pass starts its tiles from.
-            const long long t = ((long long)i * ranks + rank) * kTile + warp * kWarpGroups * kTpt;
+            const long long t = ((long long)i * ranks + rank) * kTile + (kNarrow ? 0 : warp * kWarpGroups * kTpt);
             if (carries && t % KDA_SCAN_CARRY_TOKENS == 0 && t < len && lane_ch)
                 *reinterpret_cast<L *>(carries + (size_t)carry_row(begin, n, t / KDA_SCAN_CARRY_TOKENS) * D + ch0 +
                                        lane * kLaneCh) = mine;
@@ -211,12 +218,12 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
         }
     }
     async_wait<0>();
-    if (final_state && warp == 0 && rank == 0 && lane_ch) *reinterpret_cast<L *>(final_state + state_at) = carry;
+    if (final_state && (kNarrow || warp == 0) && rank == 0 && lane_ch) *reinterpret_cast<L *>(final_state + state_at) = carry;
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
-    return launch_scan<FwdShape<XT, GT>, scan_fwd<XT, GT, kGate, kWrite>>(
+    return launch_scan<FwdShape<XT, GT>, scan_fwd<XT, GT, kGate, kWrite, false>, scan_fwd<XT, GT, kGate, kWrite, true>>(
         s, stream, static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), s.init, s.cu, static_cast<XT *>(s.out),
         s.final_state, s.carries, s.T_fixed, s.tokens, s.D);
 }

@@ -494,6 +494,13 @@ struct ScanStepArgs {
 };
 cudaError_t launch_scan_step(const ScanStepArgs &s, cudaStream_t stream);
 
+// Which sequence a CTA works on: the one that the block index gives, or the one
+// that has this place among them by length. Where every sequence fits one
+// warp's share of a tile (16 tokens, 32 of bf16 with fp32 gates), a kernel of
+// its own gives each warp one (512 sequences of 16 tokens, 4096 channels, bf16,
+// forward: 140 us with a CTA each, 49 so).
+enum ScanOrder { kOrderPlain, kOrderLongest };
+
 // What one scan kernel needs to know of a device, looked up on first use: how
 // many clusters of each size run at the same time.
 struct ScanFits {
@@ -513,10 +520,10 @@ struct ScanFits {
 // and a half rounds, the longest sequences first (24 of 65536 tokens in all,
 // 2048 channels, backward: 314 us with 1, 246 with 2, 269 with 4; forward 202
 // with 1, 145 with 2, 149 with 3, 171 with 6).
-template <typename S, auto kKernel, typename... A>
+template <typename S, auto kWide, auto kNarrow, typename... A>
 cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     static ScanFits fits;  // one for each kernel
-    const auto kernel = kKernel;
+    const auto kernel = kWide;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -524,11 +531,19 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     if (!fits.ready[dev].load(std::memory_order_acquire)) {
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)(S::smem + ClusterMaps<S::ch>::bytes(kScanMaxRanks)));
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
         if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
         fits.ready[dev].store(true, std::memory_order_release);
     }
     const int blocks = (s.D + S::ch - 1) / S::ch;
+    if (!s.cu && s.num_seqs > 1 && s.T_fixed <= S::tile / S::warps) {
+        const long long grid = (long long)((s.num_seqs + S::warps - 1) / S::warps) * blocks;
+        kNarrow<<<(unsigned)grid, S::threads, S::smem, stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
+        return cudaGetLastError();
+    }
+    const int order = s.cu && s.num_seqs > 1 && s.num_seqs <= kScanThreads ? kOrderLongest : kOrderPlain;
     const long long units = (long long)s.num_seqs * blocks;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -565,10 +580,9 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
             while (ranks > 1 && (ranks * units > 5LL * fit(1) || ranks * S::tile > mean)) ranks /= 2;
         }
     }
-    const int ordered = s.cu && s.num_seqs <= kScanThreads ? s.num_seqs : 0;
     if (err != cudaSuccess) return err;
     shape(ranks);
-    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, ordered, s.gate.lower);
+    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, s.num_seqs, order, s.gate.lower);
 }
 
 // fn<storage type, gate type, gate, write>(args, stream) for a checked call.

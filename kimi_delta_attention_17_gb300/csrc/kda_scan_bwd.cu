@@ -35,12 +35,13 @@ struct BwdShape {
     static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
-template <typename XT, typename GT, int kGate, int kWrite>
+// kNarrow: a sequence for each warp (ScanOrder).
+template <typename XT, typename GT, int kGate, int kWrite, bool kNarrow>
 __global__ void __launch_bounds__(BwdShape<XT, GT>::threads, BwdShape<XT, GT>::per_sm)
 scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict__ x,
          const GT *__restrict__ g, const float *__restrict__ carries, const int32_t *__restrict__ cu,
          XT *__restrict__ dx, GT *__restrict__ dg, float *dinit, int T_fixed, long long tokens, int D,
-         int blocks, int ranks, int ordered, float lower) {
+         int blocks, int ranks, int num_seqs, int order, float lower) {
     using S = BwdShape<XT, GT>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -53,14 +54,15 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     __shared__ __align__(16) typename S::Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
-    const int rank = ranks > 1 ? (int)cluster_rank() : 0;
+    const int rank = !kNarrow && ranks > 1 ? (int)cluster_rank() : 0;
     const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;
     int n = (int)(unit / (unsigned)blocks);
-    if (ordered > 1) n = kth_longest(cu, ordered, n, tokens, reinterpret_cast<int *>(&sh));
+    if (!kNarrow && order == kOrderLongest) n = kth_longest(cu, num_seqs, n, tokens, reinterpret_cast<int *>(&sh));
+    if (kNarrow) n = uniform(n * kWarps + warp);
     const int ch0 = (int)(unit % (unsigned)blocks) * S::ch;
     const int col = V * (tid & (kScanLanes - 1));
-    const bool has_ch = ch0 + col < D, lane_ch = ch0 + lane * kLaneCh < D;
+    const bool has_ch = ch0 + col < D && n < num_seqs, lane_ch = ch0 + lane * kLaneCh < D && n < num_seqs;
 
     // In every warp, by lane: the gradient entering the cluster's tiles from
     // behind. Read before the cluster's first barrier: dinit may be the same
@@ -69,7 +71,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     lane_set(u, 0.f);
     const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
     if (dfinal && lane_ch) u = *reinterpret_cast<const L *>(dfinal + state_at);
-    if (ranks > 1) cluster_maps_init(peers);
+    if (!kNarrow && ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
     scan_bounds(cu, n, T_fixed, tokens, begin, end);
@@ -80,7 +82,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
 
     // Of a step: tokens from this thread's first one to the sequence's end (none
     // left where negative), and the first one's element.
-    const long long t0 = ((long long)(steps - 1) * ranks + rank) * kTile + group * kTpt;
+    const long long t0 = ((long long)(steps - 1) * ranks + rank) * kTile + (kNarrow ? lane / kScanLanes : group) * kTpt;
     int left = has_ch ? (int)(len - t0) : -1;
     const int more = has_ch ? super : 0;
     size_t at = (size_t)(begin + t0) * D + ch0 + col;
@@ -192,14 +194,16 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                 }
                 cluster_maps_send(peers, steps - 1 - i, TA, TU);
             }
-            for (int v = 0; v < warp; ++v) h0 = lane_fma(sh.warp_map[p][v][0][lane], h0, sh.warp_map[p][v][1][lane]);
+            for (int v = 0; v < (kNarrow ? 0 : warp); ++v) h0 = lane_fma(sh.warp_map[p][v][0][lane], h0, sh.warp_map[p][v][1][lane]);
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
                 entry(v, 1) = h0;
                 h0 = lane_fma(A[v], h0, H[v]);
             }
             L last = u;  // the gradient entering the CTA's tile from behind
-            if (ranks > 1) {
+            if (kNarrow) {
+                u = lane_fma(sh.warp_map[p][warp][0][lane], u, sh.warp_map[p][warp][2][lane]);
+            } else if (ranks > 1) {
                 const int step = steps - 1 - i;
                 if (!cluster_maps_wait(peers, step)) lane_set(u, __uint_as_float(0x7fc00000u));
                 for (int r = ranks - 1; r >= 0; --r) {
@@ -209,12 +213,14 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                 }
             }
             L mine = last;
+            if (!kNarrow) {
 #pragma unroll
-            for (int v = kWarps - 1; v >= 0; --v) {
-                if (v == warp) mine = last;
-                if (ranks == 1 || v > 0) last = lane_fma(sh.warp_map[p][v][0][lane], last, sh.warp_map[p][v][2][lane]);
+                for (int v = kWarps - 1; v >= 0; --v) {
+                    if (v == warp) mine = last;
+                    if (ranks == 1 || v > 0) last = lane_fma(sh.warp_map[p][v][0][lane], last, sh.warp_map[p][v][2][lane]);
+                }
+                if (ranks == 1) u = last;
             }
-            if (ranks == 1) u = last;
 #pragma unroll
             for (int v = kWarpGroups - 1; v >= 0; --v) {
                 entry(v, 2) = mine;
@@ -272,12 +278,12 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
         }
     }
     async_wait<0>();
-    if (dinit && warp == 0 && rank == 0 && lane_ch) *reinterpret_cast<L *>(dinit + state_at) = u;
+    if (dinit && (kNarrow || warp == 0) && rank == 0 && lane_ch) *reinterpret_cast<L *>(dinit + state_at) = u;
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_bwd(const ScanArgs &s, cudaStream_t stream) {
-    return launch_scan<BwdShape<XT, GT>, scan_bwd<XT, GT, kGate, kWrite>>(
+    return launch_scan<BwdShape<XT, GT>, scan_bwd<XT, GT, kGate, kWrite, false>, scan_bwd<XT, GT, kGate, kWrite, true>>(
         s, stream, static_cast<const XT *>(s.dout), s.dfinal, static_cast<const XT *>(s.x),
         static_cast<const GT *>(s.g), (const float *)s.carries, s.cu, static_cast<XT *>(s.dx), static_cast<GT *>(s.dg),
         s.dinit, s.T_fixed, s.tokens, s.D);

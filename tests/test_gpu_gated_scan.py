@@ -97,6 +97,14 @@ def test_shapes(B, T, D):
     check(make(B, T, D, "bf16", "bounded", seed=B + T + D), "bounded", "norm")
 
 
+@pytest.mark.parametrize("B,T", [(2, 1), (5, 4), (3, 16), (9, 15), (5, 17), (2, 32), (7, 31), (3, 33)])
+@pytest.mark.parametrize("types", list(TYPES))
+def test_many_short_sequences(B, T, types):
+    """Around the lengths up to which each warp takes a sequence of its own (16, or 32)."""
+    check(make(B, T, 72, types, "logsigmoid", seed=B * T), "logsigmoid", "complement")
+    check(make(B, T, 264, types, "log", seed=T, init=False), "log", "norm")
+
+
 @pytest.mark.parametrize("types", list(TYPES))
 @pytest.mark.parametrize("cu", [[0, 1], [0, 0, 5, 5, 133, 134, 134], [0, 128, 256, 400], [0, 700, 701, 1400],
                                 [0, 3, 6, 9, 12, 15, 18, 21], [0, 0, 0]])
@@ -109,10 +117,37 @@ def test_no_states():
     check(make(2, 150, 16, "mixed", "log", init=False), "log", "plain")
 
 
-def test_many_packed_sequences():
-    rng = np.random.default_rng(3)
-    cu = np.concatenate([[0], np.cumsum(rng.integers(0, 40, 90))]).tolist()
-    check(make(1, cu[-1], 8, "bf16", "logsigmoid", N=90), "logsigmoid", "norm", cu=cu)
+@pytest.mark.parametrize("N,most", [(90, 40), (128, 300), (129, 9), (200, 100)])
+def test_many_packed_sequences(N, most):
+    """Up to 128 sequences are taken longest first, more in their order."""
+    rng = np.random.default_rng(N)
+    cu = np.concatenate([[0], np.cumsum(rng.integers(0, most, N))]).tolist()
+    check(make(1, cu[-1], 8, "bf16", "logsigmoid", N=N), "logsigmoid", "norm", cu=cu)
+
+
+def test_offsets_that_do_not_fit_stay_inside():
+    """Offsets past the tokens, below zero or falling are clamped: values are unspecified, memory
+    beside the outputs is not touched."""
+    T, D = 70, 16
+    v = cuda(make(1, T, D, "f32", N=4))
+    cu = torch.tensor([-5, 30, 10, 2 ** 31 - 1, 60], dtype=torch.int32, device="cuda")
+
+    def guarded(rows):
+        whole = torch.full((rows + 2, D), 7.0, device="cuda")
+        return whole, whole[1:-1]
+
+    outw, out = guarded(T)
+    finw, fin = guarded(4)
+    carw, car = guarded(T // 64 + 4)
+    gated_scan_fwd(v["x"], v["g"], v["init"], cu, out=out.view(1, T, D), final_state=fin, carries=car)
+    dxw, dx = guarded(T)
+    dgw, dg = guarded(T)
+    dinw, din = guarded(4)
+    gated_scan_bwd(v["dout"], v["x"], v["g"], car, cu, dfinal_state=v["dfinal"], dx=dx.view(1, T, D),
+                   dg=dg.view(1, T, D), dinit_state=din)
+    torch.cuda.synchronize()
+    for whole in (outw, finw, carw, dxw, dgw, dinw):
+        assert (whole[0] == 7.0).all() and (whole[-1] == 7.0).all()
 
 
 def test_rows_outside_every_sequence_stay():
