@@ -22,9 +22,9 @@
 namespace kda {
 namespace {
 
-template <typename XT, typename GT>
+template <typename XT, typename GT, int kTokens = kScanTpt<XT, GT>>
 struct FwdShape {
-    using Tiling = ScanTiling<XT, GT>;
+    using Tiling = ScanTiling<XT, GT, kTokens>;
     static constexpr int threads = kScanThreads, tpt = Tiling::tpt, vec = Tiling::vec, pairs = vec / 2;
     static constexpr int warps = threads / 32, tile = Tiling::tile, ch = Tiling::ch;
     using L = typename Lane<ch>::type;
@@ -37,18 +37,18 @@ struct FwdShape {
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
     static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
-    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
+    static constexpr int regs = vec * tpt > 32 ? 2 : vec * tpt == 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
     static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
 // kNarrow: a sequence for each warp (ScanOrder).
-template <typename XT, typename GT, int kGate, int kWrite, bool kNarrow>
-__global__ void __launch_bounds__(FwdShape<XT, GT>::threads, FwdShape<XT, GT>::per_sm)
+template <typename XT, typename GT, int kGate, int kWrite, int kTokens, bool kNarrow>
+__global__ void __launch_bounds__(kScanThreads, FwdShape<XT, GT, kTokens>::per_sm)
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
          int num_seqs, int order, float lower) {
-    using S = FwdShape<XT, GT>;
+    using S = FwdShape<XT, GT, kTokens>;
     using L = typename S::L;
     using XS = typename S::XS;
     using GS = typename S::GS;
@@ -221,11 +221,36 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     if (final_state && (kNarrow || warp == 0) && rank == 0 && lane_ch) *reinterpret_cast<L *>(final_state + state_at) = carry;
 }
 
+template <auto kValue> struct Kernel {
+    static constexpr auto value = kValue;
+};
+
+// Few long chains of bf16: what a step's composition and exchange cost shows,
+// and twice the tokens a thread halve it (one sequence of 16384 tokens, 1024
+// channels: 42 us with 4 tokens, 32 with 8; two of 8192, 2048 channels, 64
+// pairs: 46 and 45). With more pairs, or packed sequences, the CTAs that fit
+// beside one another hide it, and twice as many do with 4 (192 pairs: 106 us
+// and 117; 4 packed sequences of 2048 channels: 48 and 56).
+inline bool few_long_chains(const ScanArgs &s, int ch) {
+    const long long units = (long long)s.num_seqs * ((s.D + ch - 1) / ch);
+    return units <= 64 && (!s.cu || s.num_seqs == 1) && s.tokens / s.num_seqs >= 1024;
+}
+
 template <typename XT, typename GT, int kGate, int kWrite>
 cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
-    return launch_scan<FwdShape<XT, GT>, scan_fwd<XT, GT, kGate, kWrite, false>, scan_fwd<XT, GT, kGate, kWrite, true>>(
-        s, stream, static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), s.init, s.cu, static_cast<XT *>(s.out),
-        s.final_state, s.carries, s.T_fixed, s.tokens, s.D);
+    constexpr int kTokens = kScanTpt<XT, GT>;
+    auto launch = [&](auto shape, auto wide, auto narrow) {
+        return launch_scan<decltype(shape), wide.value, narrow.value>(
+            s, stream, static_cast<const XT *>(s.x), static_cast<const GT *>(s.g), s.init, s.cu,
+            static_cast<XT *>(s.out), s.final_state, s.carries, s.T_fixed, s.tokens, s.D);
+    };
+    using Narrow = Kernel<scan_fwd<XT, GT, kGate, kWrite, kTokens, true>>;
+    if constexpr (sizeof(XT) + sizeof(GT) == 4) {
+        if (few_long_chains(s, FwdShape<XT, GT>::ch))
+            return launch(FwdShape<XT, GT, 2 * kTokens>(), Kernel<scan_fwd<XT, GT, kGate, kWrite, 2 * kTokens, false>>(),
+                          Narrow());
+    }
+    return launch(FwdShape<XT, GT>(), Kernel<scan_fwd<XT, GT, kGate, kWrite, kTokens, false>>(), Narrow());
 }
 
 // One step: a thread per 16-byte piece of g.

@@ -273,15 +273,17 @@ __device__ __forceinline__ void store_pairs(float *to, const Pairs<V> &x) {
 // The tiling that the forward and the backward scan share: 8 threads span the
 // pieces of a row's block of channels, a warp four groups of consecutive
 // tokens, a CTA 16. 32 values a thread, 16 where all of them are fp32 and arrive
-// in twice the bytes (chosen by measurement, GB300: 128 threads against 256, 4
-// tokens against 8, each within 3 % of the best or better on every workload).
+// in twice the bytes (measured, 131072 tokens of 2048 channels, forward: bf16
+// 336 us with 32, 518 with 16 in twice the threads; bf16 with fp32 gates 346 and
+// 381; the 20011 packed fp32 tokens 62 us with 16, 63 with 32).
 constexpr int kScanThreads = 128;
 constexpr int kScanLanes = 8;                 // threads across the channels
 constexpr int kWarpGroups = 32 / kScanLanes;  // groups per warp
 template <typename XT, typename GT>
+constexpr int kScanTpt = sizeof(XT) < sizeof(GT) ? 8 : 4;  // tokens per thread
+template <typename XT, typename GT, int kTpt = kScanTpt<XT, GT>>
 struct ScanTiling {
-    static constexpr int vec = kVec<GT>;                              // channels per thread
-    static constexpr int tpt = sizeof(XT) < sizeof(GT) ? 8 : 4;       // tokens per thread
+    static constexpr int vec = kVec<GT>, tpt = kTpt;  // channels and tokens per thread
     static constexpr int groups = kScanThreads / kScanLanes, tile = groups * tpt;
     static constexpr int ch = kScanLanes * vec;                       // channels per CTA
 };
@@ -440,7 +442,9 @@ __device__ __forceinline__ void scan_bounds(const int32_t *cu, int n, int T_fixe
 }
 
 // Packed sequences are taken longest first (ties by index): the sequence whose
-// place in that order is k. All threads; up to kScanThreads sequences.
+// place in that order is k. All threads; up to kOrderedMost sequences.
+constexpr int kOrderedMost = 128;
+static_assert(kOrderedMost <= kScanThreads, "a thread ranks one sequence");
 __device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int k, long long tokens, int *lens) {
     const int tid = threadIdx.x;
     if (tid < num_seqs) {
@@ -453,10 +457,10 @@ __device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int 
         const int mine = lens[tid];
         int before = 0;
         for (int m = 0; m < num_seqs; ++m) before += lens[m] > mine || (lens[m] == mine && m < tid);
-        if (before == k) lens[kScanThreads] = tid;
+        if (before == k) lens[kOrderedMost] = tid;
     }
     __syncthreads();
-    const int n = uniform(lens[kScanThreads]);
+    const int n = uniform(lens[kOrderedMost]);
     __syncthreads();
     return n;
 }
@@ -543,7 +547,7 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
         kNarrow<<<(unsigned)grid, S::threads, S::smem, stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
         return cudaGetLastError();
     }
-    const int order = s.cu && s.num_seqs > 1 && s.num_seqs <= kScanThreads ? kOrderLongest : kOrderPlain;
+    const int order = s.cu && s.num_seqs > 1 && s.num_seqs <= kOrderedMost ? kOrderLongest : kOrderPlain;
     const long long units = (long long)s.num_seqs * blocks;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
