@@ -33,20 +33,51 @@ template <int D, typename InT, int kVar, bool kSlots>
 __global__ void __launch_bounds__(kDecodeThreads, 7)
 decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT *__restrict__ v,
                    const float *__restrict__ g, const float *__restrict__ beta, float scale,
-                   float *__restrict__ state, const int32_t *__restrict__ slots, int num_slots, int H,
+                   float *__restrict__ state, const int32_t *__restrict__ slots, int num_slots, int N, int H,
                    InT *__restrict__ out, Prologue pro) {
     constexpr bool kOpts = kVar != kDecPlain;
     if (kVar == kDecGated) pro = Prologue{KDA_DECAY_CHANNEL, KDA_GATE_LOGSIGMOID, 0.f, 1};
     constexpr int R = D / 16;  // rows per thread
-    const int nh = blockIdx.x;           // (sequence, head) flattened
-    const int col0 = blockIdx.y * kSlab;  // first state column of this slab
+    // (sequence, head) flattened, and the first state column of this slab. Over
+    // slots the grid is (head, sequence, slab and the sequences' high part): the
+    // slot is needed before anything of the state, and a division first costs.
+    int nh = blockIdx.x, col0 = blockIdx.y * kSlab, n = 0;
+    if (kSlots) {
+        constexpr int kSlabs = D / kSlab;
+        n = (int)(blockIdx.y + blockIdx.z / kSlabs * gridDim.y);
+        if (n >= N) return;
+        nh = n * H + blockIdx.x;
+        col0 = blockIdx.z % kSlabs * kSlab;
+    }
     const int tid = threadIdx.x;
     const int cq = tid & 7;   // column quad within the slab
     const int rg = tid >> 3;  // row group 0..15; rows rg + 16 m
 
+    // Token inputs of this thread's rows, in flight together (one uniform branch
+    // around g).
+    const size_t tok = (size_t)nh * D;
+    float zr[R], kin[R], qin[R];
+    const bool chan = !kOpts || pro.decay == KDA_DECAY_CHANNEL;
+    auto load_rows = [&] {
+        if (chan) {
+#pragma unroll
+            for (int m = 0; m < R; ++m) zr[m] = g[tok + rg + 16 * m];
+        }
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            kin[m] = to_f32(k[tok + rg + 16 * m]);
+            qin[m] = to_f32(q[tok + rg + 16 * m]);
+        }
+    };
+    // Over slots and with options they come before the state, beside the slot's
+    // number (256 x 32 heads of 128: 183 us after it, 181 before; the plain step
+    // 175 after, 186 before).
+    constexpr bool kRowsFirst = kSlots && kOpts;
+    if (kRowsFirst) load_rows();
+
     size_t at = nh;  // the state's place in units of d x d
     if (kSlots) {
-        const int n = nh / H, slot = slots[n];
+        const int slot = slots[n];
         if (slot < 0 || slot >= num_slots) {
             if (rg == 0) {
 #pragma unroll
@@ -54,7 +85,7 @@ decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const I
             }
             return;
         }
-        at = (size_t)slot * H + (nh - n * H);
+        at = (size_t)slot * H + blockIdx.x;
     }
     float *S = state + at * D * D + col0 + 4 * cq;
     float4 s[R];
@@ -62,22 +93,9 @@ decode_step_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const I
     for (int m = 0; m < R; ++m)
         s[m] = *reinterpret_cast<const float4 *>(S + (size_t)(rg + 16 * m) * D);
 
-    const size_t tok = (size_t)nh * D;
     // Decay of this head: per channel, one per head, or none (log a = 0).
     const float ah = kOpts && pro.decay == KDA_DECAY_SCALAR ? decay_factor(g[nh], pro) : 1.f;
-    // All row loads first (one uniform branch around g), so that they are in
-    // flight together.
-    float zr[R], kin[R], qin[R];
-    const bool chan = !kOpts || pro.decay == KDA_DECAY_CHANNEL;
-    if (chan) {
-#pragma unroll
-        for (int m = 0; m < R; ++m) zr[m] = g[tok + rg + 16 * m];
-    }
-#pragma unroll
-    for (int m = 0; m < R; ++m) {
-        kin[m] = to_f32(k[tok + rg + 16 * m]);
-        qin[m] = to_f32(q[tok + rg + 16 * m]);
-    }
+    if (!kRowsFirst) load_rows();
     float av[R], ak[R], aq[R], kr[R];
     float qk = 0.f, kss = 0.f, qss = 0.f;  // q.k and the squared norms of raw k and q
 #pragma unroll
@@ -181,7 +199,10 @@ cudaError_t launch_decode_t(const void *q, const void *k, const void *v, const f
                             const float *beta, float scale, float *state, const int32_t *slots,
                             int num_slots, void *out, int N, int H, const Prologue &pro,
                             cudaStream_t stream) {
-    dim3 grid((unsigned)(N * H), D / kSlab);
+    constexpr int kMostY = 65535;
+    const unsigned rows = (unsigned)(N < kMostY ? N : kMostY);
+    const dim3 grid = kSlots ? dim3((unsigned)H, rows, D / kSlab * ((N + rows - 1) / rows))
+                             : dim3((unsigned)(N * H), D / kSlab);
     const bool chan = pro.decay == KDA_DECAY_CHANNEL;
     const int var = chan && pro.gate == KDA_GATE_LOG && !pro.l2norm              ? kDecPlain
                     : chan && pro.gate == KDA_GATE_LOGSIGMOID && pro.l2norm ? kDecGated
@@ -189,7 +210,7 @@ cudaError_t launch_decode_t(const void *q, const void *k, const void *v, const f
 #define KDA_DECODE_LAUNCH(V)                                                                   \
     decode_step_kernel<D, InT, V, kSlots><<<grid, kDecodeThreads, 0, stream>>>(                          \
         static_cast<const InT *>(q), static_cast<const InT *>(k), static_cast<const InT *>(v), g, \
-        beta, scale, state, slots, num_slots, H, static_cast<InT *>(out), pro)
+        beta, scale, state, slots, num_slots, N, H, static_cast<InT *>(out), pro)
     switch (var) {
         case kDecPlain: KDA_DECODE_LAUNCH(kDecPlain); break;
         case kDecGated: KDA_DECODE_LAUNCH(kDecGated); break;

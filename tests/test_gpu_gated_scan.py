@@ -80,6 +80,13 @@ def test_every_form(gate, write, types):
     check(make(2, 301, 72, types, gate), gate, write)
 
 
+@pytest.mark.parametrize("write", ["plain", "complement", "norm"])
+@pytest.mark.parametrize("gate", ["log", "logsigmoid", "bounded"])
+def test_long_chains_of_bf16(gate, write):
+    """One sequence of more than 1024 tokens: 8 tokens a thread in the forward pass."""
+    check(make(1, 1333, 72, "bf16", gate, seed=7), gate, write)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 7, 8, 9, 31, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 513, 1023, 2049, 5000])
 @pytest.mark.parametrize("types", list(TYPES))
 def test_lengths(T, types):

@@ -170,6 +170,17 @@ def test_decode_by_slot_equals_dense_decode(H, d, dtype, options):
 P_OUT = 9
 
 
+def test_decode_more_rows_than_a_grid_dimension():
+    N, d = 66001, 64
+    args = [t if t is None else t.cuda() for t in decode_inputs(N, 1, d, torch.bfloat16, {})]
+    pool = torch.randn(N, 1, d, d, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) * 0.1
+    slots = torch.randperm(N, device="cuda").int()
+    state = pool[slots.long()]
+    dense = decode_step(*args, d ** -0.5, state)
+    out = decode_step(*args, d ** -0.5, pool, slots=slots)
+    assert torch.equal(out, dense) and torch.equal(pool[slots.long()], state)
+
+
 def test_decode_graph_over_slots():
     """A graph of steps whose slots are refilled between replays."""
     N, H, d, P, steps = 3, 2, 64, 8, 4
