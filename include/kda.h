@@ -511,8 +511,9 @@ size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs);
  *             returns KDA_ERR_UNSUPPORTED
  *  D          channels; a multiple of 8 (of 4 with fp32 x), i.e. rows of whole
  *             16-byte pieces, else KDA_ERR_UNSUPPORTED
- * Pointers 16-byte aligned (cu_seqlens 4-byte). No workspace. States and sums
- * are fp32; the results do not depend on the run (no atomics).
+ * Pointers 16-byte aligned (cu_seqlens 4-byte). Outputs must not overlap inputs
+ * or one another, final_state and init_state excepted. No workspace. States
+ * and sums are fp32; the results do not depend on the run (no atomics).
  */
 kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_state,
                               const int32_t *cu_seqlens, void *out, float *final_state,
@@ -537,7 +538,8 @@ kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_st
  *  dinit_state [num_seqs][D] fp32 (written), or NULL. May alias dfinal_state
  *             exactly. A zero-length sequence's is its dfinal_state (or zero).
  * With KDA_WRITE_NORM the slope of w at a = 1 (log a = 0) is unbounded; where
- * w is exactly 0 it is taken as 0. Alignment and errors as the forward call.
+ * w is exactly 0 it is taken as 0. Alignment, overlap and errors as the forward
+ * call.
  */
 kda_status kda_gated_scan_bwd(const void *dout, const float *dfinal_state, const void *x,
                               const void *g, const float *carries, const int32_t *cu_seqlens,

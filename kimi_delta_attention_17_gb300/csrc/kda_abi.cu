@@ -452,7 +452,7 @@ kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options
     s->T_fixed = T;
     if (s->tokens >= (1LL << 31) - kChunk) return KDA_ERR_INVALID_ARGUMENT;
     if (s->tokens * s->D >= (1LL << 40)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)s->num_seqs * ((s->D + 31) / 32) * kScanMaxRanks >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)s->num_seqs * ((s->D + 31) / 32) >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;  // the grid
     if (s->tokens > 0 && (!s->x || !s->g)) return KDA_ERR_INVALID_ARGUMENT;
     const void *tensors[] = {s->x,  s->g,  s->dout,        s->init,  s->dfinal, s->out,
                              s->dx, s->dg, s->final_state, s->dinit, s->carries};

@@ -4,19 +4,25 @@
 // A step is the affine map h -> A h + H with (A, H) = (a_t, w_t x_t); maps
 // compose associatively, (A, H) then (A', H') being (A' A, A' H + H'), so time
 // is cut into pieces whose maps are formed side by side and then composed in
-// order. One thread holds 8 consecutive tokens of four channels, a CTA 16 such
-// pieces of 32 channels (8 lanes across, 4 pieces per warp, 4 warps), and a
-// cluster of CTAs consecutive tiles of the same channels. The thread maps
-// are composed by shuffles in the warp, through shared memory in the CTA and
-// through distributed shared memory in the cluster; every thread then knows
-// the state that enters its piece and walks it once more, from the a and w x
-// still in its registers. Each input is read once and each output written
+// order. A thread holds 4 or 8 consecutive tokens of 4 or 8 channels, a CTA 16
+// such groups of tokens in 128 bytes of channels, and a cluster of up to 16
+// CTAs consecutive tiles of the same channels. The groups' maps are composed
+// through shared memory with a lane for each channel or two: within a warp
+// without a barrier, over the CTA's four warps after the one barrier of a step,
+// and over the cluster by asynchronous stores to one another. Each thread then
+// has the state that enters its tokens and walks them once more, from the a and
+// w x still in its registers. Each input is read once and each output written
 // once; the cluster goes on to its next tiles with the state it has reached.
 // The composition order is fixed, so the results do not depend on the run, and
 // clusters never wait for one another.
 //
-// Bound by HBM. Each thread's inputs arrive by asynchronous copies into slots
-// of its own (no barrier), one tile ahead.
+// Inputs arrive by asynchronous copies into slots of the thread's own (no
+// barrier), up to two tiles ahead. Bound by HBM where the gates are fp32
+// (131072 x 2048, bf16 x: 345 us, 6.2 TB/s); with bf16 gates the 6 bytes of a
+// value leave 20 instructions or so for it, and latency shows: 272 us, 5.9 TB/s
+// there, 77 us and 5.2 TB/s on 8 x 4096 x 2048 with the norm write. ncu, 32768
+// tokens: issue slots 47 % busy, 16 % of the warps resident (registers: a and
+// w x of 32 values a thread), the largest stall the copies' arrival.
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -31,13 +37,15 @@ struct FwdShape {
     using XS = Slots<XT, vec, tpt, threads>;
     using GS = Slots<GT, vec, tpt, threads>;
     struct Shared {
-        float map[Tiling::groups][2][ch];  // (A, H) of each group's tokens; then H gives way to the state entering them
+        // (A, H) of each group's tokens; then H gives way to the state entering them.
+        float map[Tiling::groups][2][ch];
         L warp_map[2][warps][2][32];  // (A, H) of each warp's tokens
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
     static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
-    static constexpr int regs = vec * tpt > 32 ? 2 : vec * tpt == 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
+    // CTAs that the registers hold: a and b of every value, and as many again.
+    static constexpr int regs = vec * tpt > 32 ? 2 : vec * tpt == 32 ? 4 : 6;
     static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
@@ -59,8 +67,8 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     __shared__ __align__(16) typename S::Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
-    const int rank = !kNarrow && ranks > 1 ? (int)cluster_rank() : 0;
-    const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
+    const int rank = !kNarrow && ranks > 1 ? (int)tc::cluster_rank() : 0;
+    const ClusterMaps<S::ch> peers = {reinterpret_cast<uint64_t *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;  // (sequence, channel block)
     int n = (int)(unit / (unsigned)blocks);
     if (!kNarrow && order == kOrderLongest) n = kth_longest(cu, num_seqs, n, tokens, reinterpret_cast<int *>(&sh));
@@ -75,6 +83,7 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     lane_set(carry, 0.f);
     const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
     if (init && lane_ch) carry = *reinterpret_cast<const L *>(init + state_at);
+    bool lost = false;  // a wait for the cluster gave up
     if (!kNarrow && ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
@@ -166,7 +175,7 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
             L first = carry;  // the state entering the CTA's tile
             if (kNarrow) {
                 carry = lane_fma(sh.warp_map[i & 1][warp][0][lane], carry, sh.warp_map[i & 1][warp][1][lane]);
-            } else if (!kNarrow && ranks > 1) {
+            } else if (ranks > 1) {
                 if (warp == 0) {
                     L TA, TH;
                     lane_set(TA, 1.f);
@@ -179,7 +188,8 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
                     }
                     cluster_maps_send(peers, i, TA, TH);
                 }
-                if (!cluster_maps_wait(peers, i)) lane_set(carry, __uint_as_float(0x7fc00000u));
+                cluster_maps_wait(peers, i, lost);
+                if (lost) lane_set(carry, __uint_as_float(0x7fc00000u));
                 for (int r = 0; r < ranks; ++r) {
                     if (r == rank) first = carry;
                     const auto m = peers.map(i, r);
@@ -253,7 +263,9 @@ cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
     return launch(FwdShape<XT, GT>(), Kernel<scan_fwd<XT, GT, kGate, kWrite, kTokens, false>>(), Narrow());
 }
 
-// One step: a thread per 16-byte piece of g.
+// One step: a thread per 16-byte piece of g, every load issued before the first
+// use. Bound by HBM (2048 rows of 4096 channels out of a pool of twice as many:
+// 22.6 us, 5.9 TB/s) or by the launch.
 constexpr int kStepThreads = 128;
 template <typename XT, typename GT, int kGate, int kWrite>
 __global__ void __launch_bounds__(kStepThreads)
@@ -263,12 +275,12 @@ scan_step(const XT *__restrict__ x, const GT *__restrict__ g, float *__restrict_
     constexpr int V = kVec<GT>;
     const long long i = (long long)blockIdx.x * kStepThreads + threadIdx.x;
     if (i >= pieces) return;
-    const int n = (int)(i / per_row), c = (int)(i % per_row) * V;
+    const int n = (int)(i / per_row), ch = (int)(i % per_row) * V;
     const long long slot = slots ? slots[n] : n;
     const size_t at = (size_t)i * V;
     Pairs<V> h = {};
     if (slot >= 0 && slot < num_slots) {
-        float *sp = state + (size_t)slot * per_row * V + c;
+        float *sp = state + (size_t)slot * per_row * V + ch;
         h = load_pairs<V>(sp);
         const Pairs<V> xv = load_pairs<V>(x + at), zv = load_pairs<V>(g + at);
 #pragma unroll

@@ -5,9 +5,9 @@
 #include <atomic>
 
 #include "kda_internal.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
-
 
 // Validated kda_scan_options.
 struct ScanGate {
@@ -26,8 +26,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-constexpr float kLog2E = 1.44269504088896341f;
-
 __device__ __forceinline__ float sqrt_approx(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -43,6 +41,7 @@ __device__ __forceinline__ float max_nan(float x, float y) {  // NaN stays NaN
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
+constexpr float kLog2E = 1.44269504088896341f;
 
 // Two fp32 values that one instruction takes together (FFMA2 and its kin): the
 // scans are short of issue slots before they are short of anything else.
@@ -334,15 +333,6 @@ __device__ __forceinline__ void async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The exchange of tile maps between the CTAs of a cluster. Each step every CTA
 // sends its map (two values per channel) to every CTA, itself included, by
 // asynchronous stores that the receiver's mbarrier counts: no fence, which
@@ -357,22 +347,21 @@ struct ClusterMaps {
     };
     // In shared memory: two mbarriers, then [2][ranks][32] maps.
     static constexpr size_t bytes(int ranks) { return ranks > 1 ? 16 + 2 * ranks * 32 * sizeof(Map) : 0; }
-    unsigned long long *bar;
+    uint64_t *bar;
     int rank, ranks;
     __device__ __forceinline__ Map &map(int step, int r) const {
         return reinterpret_cast<Map *>(bar + 2)[((step & 1) * ranks + r) * 32 + (threadIdx.x & 31)];
     }
 };
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // All threads of the cluster, once.
 template <int kCh>
 __device__ __forceinline__ void cluster_maps_init(const ClusterMaps<kCh> &m) {
     if (threadIdx.x == 0) {
-        for (int b = 0; b < 2; ++b)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&m.bar[b])) : "memory");
+        tc::mbar_init(&m.bar[0], 1);
+        tc::mbar_init(&m.bar[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    cluster_sync();
+    tc::cluster_sync();
 }
 __device__ __forceinline__ void send_async(uint32_t to, uint32_t bar, float a, float b) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(a),
@@ -388,36 +377,17 @@ __device__ __forceinline__ void send_async(uint32_t to, uint32_t bar, F2 a, F2 b
 template <int kCh>
 __device__ __forceinline__ void cluster_maps_send(const ClusterMaps<kCh> &m, int step, typename Lane<kCh>::type a,
                                                   typename Lane<kCh>::type b) {
-    const uint32_t bar = smem_addr(&m.bar[step & 1]), mine = smem_addr(&m.map(step, m.rank));
-    if ((threadIdx.x & 31) == 0)
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                     "r"(m.ranks * 32 * (int)sizeof(typename ClusterMaps<kCh>::Map))
-                     : "memory");
-    for (int r = 0; r < m.ranks; ++r) {
-        uint32_t to, to_bar;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(r));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(bar), "r"(r));
-        send_async(to, to_bar, a, b);
-    }
+    uint64_t *bar = &m.bar[step & 1];
+    const auto *mine = &m.map(step, m.rank);
+    if ((threadIdx.x & 31) == 0) tc::mbar_expect_tx(bar, m.ranks * 32 * (int)sizeof(*mine));
+    for (int r = 0; r < m.ranks; ++r) send_async(tc::cluster_addr(mine, r), tc::cluster_addr(bar, r), a, b);
 }
-// Waits for the maps of step `step`. The wait always ends (the CTAs of a cluster
-// run together and send as many maps); should it not within its bound, false
-// is returned and the caller's results become NaN.
+// Waits for the maps of step `step`. The wait always ends: the CTAs of a cluster
+// run together and send as many maps. Should it not within its bound, `lost`
+// is set, the call waits for nothing more, and its results become NaN.
 template <int kCh>
-__device__ __forceinline__ bool cluster_maps_wait(const ClusterMaps<kCh> &m, int step) {
-    const uint32_t bar = smem_addr(&m.bar[step & 1]);
-    for (int polls = 0; polls < (1 << 22); ++polls) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"((uint32_t)(step >> 1) & 1u)
-            : "memory");
-        if (__all_sync(0xffffffffu, done)) return true;
-    }
-    return false;
+__device__ __forceinline__ void cluster_maps_wait(const ClusterMaps<kCh> &m, int step, bool &lost) {
+    if (!lost && !tc::mbar_wait_cluster(&m.bar[step & 1], (uint32_t)(step >> 1) & 1u, 1u << 20)) lost = true;
 }
 
 // A value that is the same in every lane, so that the compiler knows: it then
@@ -505,12 +475,11 @@ cudaError_t launch_scan_step(const ScanStepArgs &s, cudaStream_t stream);
 // forward: 140 us with a CTA each, 49 so).
 enum ScanOrder { kOrderPlain, kOrderLongest };
 
-// What one scan kernel needs to know of a device, looked up on first use: how
-// many clusters of each size run at the same time.
+// How many clusters of each size of one kernel run at the same time on a device,
+// looked up on first use.
 struct ScanFits {
     static constexpr int kDevices = 64;
     std::atomic<int> clusters[kDevices][kScanMaxRanks + 1];  // 0: not looked up
-    std::atomic<bool> ready[kDevices];                       // the kernel's attributes are set
 };
 
 // Launches a scan over the (sequence, channel block) pairs. CTAs per cluster:
@@ -532,21 +501,18 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if (dev >= ScanFits::kDevices) return cudaErrorInvalidDevice;
-    if (!fits.ready[dev].load(std::memory_order_acquire)) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)(S::smem + ClusterMaps<S::ch>::bytes(kScanMaxRanks)));
-        if (err == cudaSuccess)
-            err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
-        if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (err != cudaSuccess) return err;
-        fits.ready[dev].store(true, std::memory_order_release);
-    }
     const int blocks = (s.D + S::ch - 1) / S::ch;
     if (!s.cu && s.num_seqs > 1 && s.T_fixed <= S::tile / S::warps) {
         const long long grid = (long long)((s.num_seqs + S::warps - 1) / S::warps) * blocks;
+        err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+        if (err != cudaSuccess) return err;
         kNarrow<<<(unsigned)grid, S::threads, S::smem, stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
         return cudaGetLastError();
     }
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(S::smem + ClusterMaps<S::ch>::bytes(kScanMaxRanks)));
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err != cudaSuccess) return err;
     const int order = s.cu && s.num_seqs > 1 && s.num_seqs <= kOrderedMost ? kOrderLongest : kOrderPlain;
     const long long units = (long long)s.num_seqs * blocks;
     cudaLaunchAttribute attr[1];

@@ -7,9 +7,14 @@
 // a cluster of CTAs over consecutive tiles, which here goes through the
 // sequence from its end. dg needs h_{t-1} as well; it is formed again within
 // the tile by the forward composition, from the fp32 state that the forward
-// call saved at the tile's first token, so neither h nor a second pass over the sequence is read, and h is
-// not taken from its rounded outputs. Bound by HBM: x, g and dout in, dx and
-// dg out, once each.
+// call saved at the tile's first token, so neither h nor a second pass over the
+// sequence is read, and h is not taken from its rounded outputs. x, g and dout
+// come in and dx and dg go out once each.
+//
+// The gates' slopes are formed after the exchange, from a and 1 - a kept in
+// registers. Bound by HBM with fp32 gates (131072 x 2048, bf16 x: 571 us, 6.6
+// TB/s); with bf16 gates by latency at 11 % of the warps resident (578 us, 4.6
+// TB/s; 8 x 4096 x 2048 with the norm write 137 us, 4.9 TB/s).
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -25,13 +30,15 @@ struct BwdShape {
     using XS = Slots<XT, vec, tpt, threads>;
     using GS = Slots<GT, vec, tpt, threads>;
     struct Shared {
-        float map[Tiling::groups][3][ch];     // A, H, U of each group's tokens; then the state and the gradient entering them
+        // A, H, U of each group's tokens; then the state and the gradient entering them.
+        float map[Tiling::groups][3][ch];
         L warp_map[2][warps][3][32];  // A, H, U of each warp's tokens
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (2 * XS::bytes_per_stage + GS::bytes_per_stage);
     static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
-    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;  // CTAs that the registers hold: a and b of every element, and as many again
+    // CTAs that the registers hold: a and b of every value, and as many again.
+    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;
     static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
 };
 
@@ -54,8 +61,8 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     __shared__ __align__(16) typename S::Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5), group = tid / kScanLanes;
-    const int rank = !kNarrow && ranks > 1 ? (int)cluster_rank() : 0;
-    const ClusterMaps<S::ch> peers = {reinterpret_cast<unsigned long long *>(smem_raw + S::smem), rank, ranks};
+    const int rank = !kNarrow && ranks > 1 ? (int)tc::cluster_rank() : 0;
+    const ClusterMaps<S::ch> peers = {reinterpret_cast<uint64_t *>(smem_raw + S::smem), rank, ranks};
     const unsigned unit = blockIdx.x / (unsigned)ranks;
     int n = (int)(unit / (unsigned)blocks);
     if (!kNarrow && order == kOrderLongest) n = kth_longest(cu, num_seqs, n, tokens, reinterpret_cast<int *>(&sh));
@@ -71,6 +78,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     lane_set(u, 0.f);
     const size_t state_at = (size_t)n * D + ch0 + lane * kLaneCh;
     if (dfinal && lane_ch) u = *reinterpret_cast<const L *>(dfinal + state_at);
+    bool lost = false;  // a wait for the cluster gave up
     if (!kNarrow && ranks > 1) cluster_maps_init(peers);
 
     long long begin, end;
@@ -205,7 +213,8 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                 u = lane_fma(sh.warp_map[p][warp][0][lane], u, sh.warp_map[p][warp][2][lane]);
             } else if (ranks > 1) {
                 const int step = steps - 1 - i;
-                if (!cluster_maps_wait(peers, step)) lane_set(u, __uint_as_float(0x7fc00000u));
+                cluster_maps_wait(peers, step, lost);
+                if (lost) lane_set(u, __uint_as_float(0x7fc00000u));
                 for (int r = ranks - 1; r >= 0; --r) {
                     if (r == rank) last = u;
                     const auto m = peers.map(step, r);

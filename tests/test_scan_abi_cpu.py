@@ -47,7 +47,7 @@ def test_scan_refusals(L, call, tensors):
         assert call(L, D=8, **{t: None}) == INVALID
     for bad in (dict(B=0), dict(T=-1), dict(D=0), dict(D=-4), dict(N=0), dict(N=2), dict(dt=2), dict(gdt=-1),
                 dict(cu=FAKE, B=2, N=2), dict(cu=FAKE + 2), dict(T=2 ** 31 - 1), dict(B=2 ** 20, T=2 ** 12, N=2 ** 20),
-                dict(T=2 ** 22, D=2 ** 18), dict(B=2 ** 28, N=2 ** 28, T=1), dict(o=opts(gate=3)),
+                dict(T=2 ** 22, D=2 ** 18), dict(B=2 ** 19, N=2 ** 19, T=0, D=2 ** 18), dict(o=opts(gate=3)),
                 dict(o=opts(write=3)), dict(o=opts(write=-1)), dict(o=opts(gate=2, lower=0.0)),
                 dict(o=opts(gate=2, lower=-11.0)), dict(o=opts(gate=2, lower=float("nan")))):
         assert call(L, **bad) == INVALID, bad
