@@ -43,10 +43,11 @@ struct FwdShape {
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (XS::bytes_per_stage + GS::bytes_per_stage);
-    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
-    // CTAs that the registers hold: a and b of every value, and as many again.
-    static constexpr int regs = vec * tpt > 32 ? 2 : vec * tpt == 32 ? 4 : 6;
-    static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
+    // CTAs per SM that the registers are shared out for. Fewer than the shared
+    // memory would hold is faster where a thread has 32 values (fp32 gates, 16
+    // rows of 2048 x 2048: 106 us with 4, 93 with 3; bf16 gates 72 with 4, 82 with
+    // 3; all fp32, 20011 packed tokens: 62 with 5, 60 with 4).
+    static constexpr int per_sm = vec * tpt > 32 ? 2 : sizeof(XT) < sizeof(GT) ? 3 : 4;
 };
 
 // kNarrow: a sequence for each warp (ScanOrder).

@@ -287,7 +287,6 @@ struct ScanTiling {
     static constexpr int ch = kScanLanes * vec;                       // channels per CTA
 };
 constexpr int kScanMaxRanks = 16;
-constexpr size_t kSmSmem = 228 * 1024, kCtaReserved = 1024;  // shared memory of an SM, and what each CTA takes beside its own
 
 // The slots of shared memory that a thread's tokens arrive in, [stage][token of
 // the thread][thread]: each thread copies what it reads itself.

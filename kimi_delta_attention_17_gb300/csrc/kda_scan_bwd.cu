@@ -36,10 +36,10 @@ struct BwdShape {
     };
     static constexpr int stages = 2;
     static constexpr size_t smem = stages * (2 * XS::bytes_per_stage + GS::bytes_per_stage);
-    static constexpr int fit = (int)(kSmSmem / (smem + sizeof(Shared) + kCtaReserved));
-    // CTAs that the registers hold: a and b of every value, and as many again.
-    static constexpr int regs = vec * tpt >= 32 ? 4 : 6;
-    static constexpr int per_sm = fit < regs ? fit : regs;  // CTAs
+    // CTAs per SM that the registers are shared out for: with fp32 gates fewer than
+    // the shared memory would hold (16 rows of 2048 x 2048: 208 us with 3, 160 with
+    // 2; bf16 gates 141 and 135, but 130 with 3 in clusters; all fp32 215 and 218).
+    static constexpr int per_sm = sizeof(XT) < sizeof(GT) ? 2 : 3;
 };
 
 // kNarrow: a sequence for each warp (ScanOrder).
