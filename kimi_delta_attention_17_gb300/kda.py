@@ -2,7 +2,6 @@
 torch CUDA tensors. It only marshals arguments (pointers, sizes, the current
 stream) and allocates outputs and scratch with torch when the caller does not
 pass them; every step of the computation runs in the library's kernels."""
-import contextlib
 import ctypes
 
 import torch
@@ -161,26 +160,29 @@ def chunk_fwd(q, k, v, g, beta, scale, init_state=None, cu_seqlens=None, *, out=
 # object around it, 2 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
-_HERE = contextlib.nullcontext()
 
 
-def _scope(device, stream):
-    """Context in which allocations and launches of a call on ``device``'s
-    tensors belong to its stream (the device's current one when None)."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream must belong to the tensors' device")
-        return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
-        return _HERE
-    return torch.cuda.device(device)
-
-
-def _same_device(first, **others):
-    index = first.get_device()
-    for name, t in others.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError("%s must be on the same device as the other tensors" % name)
+def _on_stream(call, tensors, stream, *args):
+    """call(*args) where allocations and launches belong to the tensors' device and
+    to ``stream`` (the device's current one when None). ``tensors``: name ->
+    tensor or None, the first one not None."""
+    index = -1
+    for name, t in tensors.items():
+        if t is not None:
+            i = t.get_device()
+            if index < 0:
+                index = i
+            elif i != index:
+                raise ValueError("%s must be on the same device as the other tensors" % name)
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(*args, _raw_stream(index))
+        with torch.cuda.device(index):
+            return call(*args, _raw_stream(index))
+    if stream.device.index != index:
+        raise ValueError("stream must belong to the tensors' device")
+    with torch.cuda.stream(stream):
+        return call(*args, stream.cuda_stream)
 
 
 def decode_step(q, k, v, g, beta, scale, state, *, out=None, stream=None, decay="channel",
@@ -224,31 +226,39 @@ def decode_step(q, k, v, g, beta, scale, state, *, out=None, stream=None, decay=
 
 def _decode_step_slots(q, k, v, g, beta, scale, state, slots, out, stream, opts, decay):
     """decode_step over a pool; its tensors are checked for type, not yet for shape."""
-    N, H, dk = q.shape
-    dv = v.shape[-1]
     _need(slots, "slots", torch.int32, 1)
-    if k.shape != q.shape or v.shape[:2] != q.shape[:2] or beta.shape != q.shape[:2]:
+    shape = q.shape
+    N, H, dk = shape
+    rows, dv = (N, H), v.shape[2]
+    if k.shape != shape or v.shape[:2] != rows or beta.shape != rows:
         raise ValueError("q, k, v and beta must share [N, H]")
-    if decay != "none" and g.shape != (q.shape if decay == "channel" else q.shape[:2]):
+    if decay != "none" and g.shape != (shape if decay == "channel" else rows):
         raise ValueError("g must be [N, H, dk], or [N, H] with the scalar decay")
     if slots.shape[0] != N:
         raise ValueError("slots must have one entry per row")
     if state.shape[1:] != (H, dk, dv):
         raise ValueError("state must be [P, H, dk, dv]")
-    _same_device(q, k=k, v=v, g=g if decay != "none" else None, beta=beta, state=state, slots=slots,
-                 out=out)
-    with _scope(q.device, stream):
-        if out is None:
-            out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-        else:
-            _need(out, "out", q.dtype, 3)
-            if out.shape != v.shape:
-                raise ValueError("out must have v's shape")
-        _lib.check("kda_decode_step_slots", _lib.lib().kda_decode_step_slots(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state), _ptr(slots),
-            _ptr(out), N, state.shape[0], H, dk, dv, _DTYPES[q.dtype],
-            None if opts is None else ctypes.byref(opts),
-            _raw_stream(q.get_device())))
+    if out is not None:
+        _need(out, "out", q.dtype, 3)
+        if out.shape != v.shape:
+            raise ValueError("out must have v's shape")
+    return _on_stream(_launch_decode_slots,
+                      {"q": q, "k": k, "v": v, "g": g if decay != "none" else None, "beta": beta,
+                       "state": state, "slots": slots, "out": out},
+                      stream, q, k, v, g, beta, scale, state, slots, out, opts)
+
+
+def _launch_decode_slots(q, k, v, g, beta, scale, state, slots, out, opts, stream):
+    if out is None:
+        out = torch.empty_like(v)
+    N, H, dk = q.shape
+    status = _lib.lib().kda_decode_step_slots(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if g is None else g.data_ptr(),
+        beta.data_ptr(), scale, state.data_ptr(), slots.data_ptr(), out.data_ptr(), N,
+        state.shape[0], H, dk, v.shape[-1], _DTYPES[q.dtype],
+        None if opts is None else ctypes.byref(opts), stream)
+    if status:
+        _lib.check("kda_decode_step_slots", status)
     return out
 
 

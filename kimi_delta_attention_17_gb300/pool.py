@@ -4,21 +4,21 @@ gated_scan_step take it with ``slots``, or [L, P, ...] over L layers."""
 import torch
 
 from . import _lib
-from .kda import _need, _ptr, _raw_stream, _same_device, _scope
+from .kda import _need, _on_stream, _ptr
 
 
 def _pool(t, name, slot_dim):
     """Checks a pool; returns (layers, slots, bytes per slot)."""
     _need(t, name)
-    if slot_dim not in (0, 1):
+    if slot_dim != 0 and slot_dim != 1:
         raise ValueError("slot_dim must be 0 (a pool [P, ...]) or 1 ([L, P, ...])")
-    if t.dim() < slot_dim + 2:
+    shape, size = t.shape, t.numel()
+    if len(shape) < slot_dim + 2:
         raise ValueError("%s must be [%sP, ...]" % (name, "L, " if slot_dim else ""))
-    layers = t.shape[0] if slot_dim else 1
-    slots = t.shape[slot_dim]
-    if t.numel() == 0:
+    if size == 0:
         raise ValueError("%s must not be empty" % name)
-    return layers, slots, t.element_size() * (t.numel() // (layers * slots))
+    layers, slots = shape[0] if slot_dim else 1, shape[slot_dim]
+    return layers, slots, t.element_size() * (size // (layers * slots))
 
 
 def state_copy(pool, src, dst, *, source=None, slot_dim=0, stream=None):
@@ -48,12 +48,17 @@ def state_copy(pool, src, dst, *, source=None, slot_dim=0, stream=None):
             raise ValueError("source must have the pool's layers and slot shape")
         if source.data_ptr() == pool.data_ptr() and source_slots == slots:
             source = None
-    _same_device(pool, src=src, dst=dst, source=source)
-    with _scope(pool.device, stream):
-        _lib.check("kda_state_copy", _lib.lib().kda_state_copy(
-            _ptr(source), source_slots, _ptr(pool), slots, _ptr(src), _ptr(dst), src.shape[0],
-            layers, nbytes, _raw_stream(pool.get_device())))
+    _on_stream(_launch_copy, {"pool": pool, "src": src, "dst": dst, "source": source}, stream, pool,
+               src, dst, source, source_slots, slots, layers, nbytes)
     return pool
+
+
+def _launch_copy(pool, src, dst, source, source_slots, slots, layers, nbytes, stream):
+    status = _lib.lib().kda_state_copy(
+        _ptr(source), source_slots, pool.data_ptr(), slots, src.data_ptr(), dst.data_ptr(),
+        src.shape[0], layers, nbytes, stream)
+    if status:
+        _lib.check("kda_state_copy", status)
 
 
 def state_compact(pool, live, *, slot_dim=0, new_slot=None, count=None, stream=None):
@@ -73,15 +78,22 @@ def state_compact(pool, live, *, slot_dim=0, new_slot=None, count=None, stream=N
             _need(t, name, torch.int32, 1)
             if t.shape[0] != n:
                 raise ValueError("%s must be int32 [%d]" % (name, n))
-    _same_device(pool, live=live, new_slot=new_slot, count=count)
-    with _scope(pool.device, stream):
-        if new_slot is None:
-            new_slot = torch.empty(slots, dtype=torch.int32, device=pool.device)
-        if count is None:
-            count = torch.empty(1, dtype=torch.int32, device=pool.device)
-        need = int(_lib.lib().kda_state_compact_workspace_size(slots))
-        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device) if need else None
-        _lib.check("kda_state_compact", _lib.lib().kda_state_compact(
-            _ptr(pool), slots, _ptr(live), _ptr(new_slot), _ptr(count), layers, nbytes,
-            _ptr(workspace), need, _raw_stream(pool.get_device())))
+    return _on_stream(_launch_compact,
+                      {"pool": pool, "live": live, "new_slot": new_slot, "count": count}, stream, pool,
+                      live, new_slot, count, slots, layers, nbytes)
+
+
+def _launch_compact(pool, live, new_slot, count, slots, layers, nbytes, stream):
+    if new_slot is None:
+        new_slot = torch.empty(slots, dtype=torch.int32, device=pool.device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=pool.device)
+    lib = _lib.lib()
+    need = lib.kda_state_compact_workspace_size(slots)
+    workspace = torch.empty(need, dtype=torch.uint8, device=pool.device) if need else None
+    status = lib.kda_state_compact(
+        pool.data_ptr(), slots, live.data_ptr(), new_slot.data_ptr(), count.data_ptr(), layers, nbytes,
+        _ptr(workspace), need, stream)
+    if status:
+        _lib.check("kda_state_compact", status)
     return new_slot, count

@@ -7,7 +7,7 @@ import functools
 import torch
 
 from . import _lib
-from .kda import _DTYPES, _need, _ptr, _raw_stream, _same_device, _scope
+from .kda import _DTYPES, _need, _on_stream, _ptr
 
 
 @functools.lru_cache(maxsize=64)
@@ -50,24 +50,26 @@ def _tokens(x, g, cu_seqlens):
 
 
 def _states(t, name, N, x):
-    """A states tensor [N, channels...] fp32, or None."""
-    if t is not None:
-        _need(t, name, torch.float32)
-        if t.shape != (N,) + x.shape[2:]:
-            raise ValueError("%s must be [%d, %s]" % (name, N, ", ".join(map(str, x.shape[2:]))))
-    return t
+    """Checks a states tensor [N, channels...] fp32."""
+    _need(t, name, torch.float32)
+    if t.shape != (N,) + x.shape[2:]:
+        raise ValueError("%s must be [%d, %s]" % (name, N, ", ".join(map(str, x.shape[2:]))))
 
 
 def _like(t, name, of, what):
-    if t is not None:
-        _need(t, name, of.dtype)
-        if t.shape != of.shape:
-            raise ValueError("%s must have %s's shape" % (name, what))
-    return t
+    _need(t, name, of.dtype)
+    if t.shape != of.shape:
+        raise ValueError("%s must have %s's shape" % (name, what))
 
 
 def _carry_rows(B, T, N):
     return B * T // _lib.SCAN_CARRY_TOKENS + N
+
+
+def _carries(t, B, T, N, D):
+    _need(t, "carries", torch.float32, 2)
+    if t.shape != (_carry_rows(B, T, N), D):
+        raise ValueError("carries must be [%d, %d]" % (_carry_rows(B, T, N), D))
 
 
 def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_state=None,
@@ -89,27 +91,34 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
     Rows of ``out`` outside every sequence are left as they were."""
     B, T, D, N = _tokens(x, g, cu_seqlens)
     opts = _scan_options(gate, gate_lower, write)
-    _states(init_state, "init_state", N, x)
-    _states(final_state, "final_state", N, x)
-    _like(out, "out", x, "x")
-    rows = _carry_rows(B, T, N)
+    if init_state is not None:
+        _states(init_state, "init_state", N, x)
+    if final_state is not None:
+        _states(final_state, "final_state", N, x)
+    if out is not None:
+        _like(out, "out", x, "x")
     if carries is not None:
-        _need(carries, "carries", torch.float32, 2)
-        if carries.shape != (rows, D):
-            raise ValueError("carries must be [%d, %d]" % (rows, D))
-    _same_device(x, g=g, init_state=init_state, cu_seqlens=cu_seqlens, out=out,
-                 final_state=final_state, carries=carries)
-    with _scope(x.device, stream):
-        if out is None:
-            out = torch.empty_like(x)
-        if final_state is None and output_final_state:
-            final_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
-        if carries is None and save_carries:
-            carries = torch.empty((rows, D), dtype=torch.float32, device=x.device)
-        _lib.check("kda_gated_scan_fwd", _lib.lib().kda_gated_scan_fwd(
-            _ptr(x), _ptr(g), _ptr(init_state), _ptr(cu_seqlens), _ptr(out), _ptr(final_state),
-            _ptr(carries), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype], opts,
-            _raw_stream(x.get_device())))
+        _carries(carries, B, T, N, D)
+    return _on_stream(_launch_fwd,
+                      {"x": x, "g": g, "init_state": init_state, "cu_seqlens": cu_seqlens, "out": out,
+                       "final_state": final_state, "carries": carries},
+                      stream, x, g, init_state, cu_seqlens, out, final_state, carries, save_carries,
+                      output_final_state, B, T, D, N, opts)
+
+
+def _launch_fwd(x, g, init_state, cu_seqlens, out, final_state, carries, save_carries,
+                output_final_state, B, T, D, N, opts, stream):
+    if out is None:
+        out = torch.empty_like(x)
+    if final_state is None and output_final_state:
+        final_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
+    if carries is None and save_carries:
+        carries = torch.empty((_carry_rows(B, T, N), D), dtype=torch.float32, device=x.device)
+    status = _lib.lib().kda_gated_scan_fwd(
+        x.data_ptr(), g.data_ptr(), _ptr(init_state), _ptr(cu_seqlens), out.data_ptr(),
+        _ptr(final_state), _ptr(carries), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype], opts, stream)
+    if status:
+        _lib.check("kda_gated_scan_fwd", status)
     return out, final_state, carries
 
 
@@ -123,28 +132,35 @@ def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, d
     B, T, D, N = _tokens(x, g, cu_seqlens)
     opts = _scan_options(gate, gate_lower, write)
     _like(dout, "dout", x, "x")
-    if dout is None:
-        raise TypeError("dout must be a torch.Tensor")
-    _need(carries, "carries", torch.float32, 2)
-    if carries.shape != (_carry_rows(B, T, N), D):
-        raise ValueError("carries must be [%d, %d]" % (_carry_rows(B, T, N), D))
-    _states(dfinal_state, "dfinal_state", N, x)
-    _states(dinit_state, "dinit_state", N, x)
-    _like(dx, "dx", x, "x")
-    _like(dg, "dg", g, "g")
-    _same_device(x, g=g, dout=dout, carries=carries, cu_seqlens=cu_seqlens,
-                 dfinal_state=dfinal_state, dinit_state=dinit_state, dx=dx, dg=dg)
-    with _scope(x.device, stream):
-        if dx is None:
-            dx = torch.empty_like(x)
-        if dg is None:
-            dg = torch.empty_like(g)
-        if dinit_state is None and output_dinit_state:
-            dinit_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
-        _lib.check("kda_gated_scan_bwd", _lib.lib().kda_gated_scan_bwd(
-            _ptr(dout), _ptr(dfinal_state), _ptr(x), _ptr(g), _ptr(carries), _ptr(cu_seqlens),
-            _ptr(dx), _ptr(dg), _ptr(dinit_state), B, T, D, N, _DTYPES[x.dtype], _DTYPES[g.dtype],
-            opts, _raw_stream(x.get_device())))
+    _carries(carries, B, T, N, D)
+    for t, name in ((dfinal_state, "dfinal_state"), (dinit_state, "dinit_state")):
+        if t is not None:
+            _states(t, name, N, x)
+    if dx is not None:
+        _like(dx, "dx", x, "x")
+    if dg is not None:
+        _like(dg, "dg", g, "g")
+    return _on_stream(_launch_bwd,
+                      {"x": x, "g": g, "dout": dout, "carries": carries, "cu_seqlens": cu_seqlens,
+                       "dfinal_state": dfinal_state, "dinit_state": dinit_state, "dx": dx, "dg": dg},
+                      stream, dout, x, g, carries, cu_seqlens, dfinal_state, dx, dg, dinit_state,
+                      output_dinit_state, B, T, D, N, opts)
+
+
+def _launch_bwd(dout, x, g, carries, cu_seqlens, dfinal_state, dx, dg, dinit_state,
+                output_dinit_state, B, T, D, N, opts, stream):
+    if dx is None:
+        dx = torch.empty_like(x)
+    if dg is None:
+        dg = torch.empty_like(g)
+    if dinit_state is None and output_dinit_state:
+        dinit_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
+    status = _lib.lib().kda_gated_scan_bwd(
+        dout.data_ptr(), _ptr(dfinal_state), x.data_ptr(), g.data_ptr(), carries.data_ptr(),
+        _ptr(cu_seqlens), dx.data_ptr(), dg.data_ptr(), _ptr(dinit_state), B, T, D, N,
+        _DTYPES[x.dtype], _DTYPES[g.dtype], opts, stream)
+    if status:
+        _lib.check("kda_gated_scan_bwd", status)
     return dx, dg, dinit_state
 
 
@@ -159,7 +175,7 @@ def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log
     N, D = _rows(x, g, 1)
     opts = _scan_options(gate, gate_lower, write)
     _need(state, "state", torch.float32)
-    if state.shape[1:] != x.shape[1:] or state.dim() != x.dim():
+    if state.shape[1:] != x.shape[1:]:
         raise ValueError("state must be [slots, %s]" % ", ".join(map(str, x.shape[1:])))
     if slots is None:
         if state.shape[0] != N:
@@ -168,13 +184,18 @@ def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log
         _need(slots, "slots", torch.int32, 1)
         if slots.shape[0] != N:
             raise ValueError("slots must have one entry per row")
-    _like(out, "out", x, "x")
-    _same_device(x, g=g, state=state, slots=slots, out=out)
-    with _scope(x.device, stream):
-        if out is None:
-            out = torch.empty_like(x)
-        _lib.check("kda_gated_scan_step", _lib.lib().kda_gated_scan_step(
-            _ptr(x), _ptr(g), _ptr(state), _ptr(slots), _ptr(out), N, state.shape[0], D,
-            _DTYPES[x.dtype], _DTYPES[g.dtype], opts,
-            _raw_stream(x.get_device())))
+    if out is not None:
+        _like(out, "out", x, "x")
+    return _on_stream(_launch_step, {"x": x, "g": g, "state": state, "slots": slots, "out": out}, stream,
+                      x, g, state, slots, out, N, D, opts)
+
+
+def _launch_step(x, g, state, slots, out, N, D, opts, stream):
+    if out is None:
+        out = torch.empty_like(x)
+    status = _lib.lib().kda_gated_scan_step(
+        x.data_ptr(), g.data_ptr(), state.data_ptr(), _ptr(slots), out.data_ptr(), N, state.shape[0],
+        D, _DTYPES[x.dtype], _DTYPES[g.dtype], opts, stream)
+    if status:
+        _lib.check("kda_gated_scan_step", status)
     return out
