@@ -478,7 +478,7 @@ enum ScanOrder { kOrderPlain, kOrderLongest };
 // looked up on first use.
 struct ScanFits {
     static constexpr int kDevices = 64;
-    std::atomic<int> clusters[kDevices][kScanMaxRanks + 1];  // 0: not looked up
+    std::atomic<int> clusters[kDevices][kScanMaxRanks + 1];  // the number and 1; 0: not looked up
 };
 
 // Launches a scan over the (sequence, channel block) pairs. CTAs per cluster:
@@ -528,13 +528,12 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
         cfg.dynamicSmemBytes = S::smem + ClusterMaps<S::ch>::bytes(ranks);
     };
     auto fit = [&](int ranks) {  // clusters of this size at the same time
-        int n = fits.clusters[dev][ranks].load(std::memory_order_relaxed);
-        if (n > 0) return n;
+        int n = fits.clusters[dev][ranks].load(std::memory_order_relaxed) - 1;
+        if (n >= 0) return n;
         shape(ranks);
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
         if (e != cudaSuccess) err = e;
-        n = n > 0 ? n : 1;
-        if (e == cudaSuccess) fits.clusters[dev][ranks].store(n, std::memory_order_relaxed);
+        else fits.clusters[dev][ranks].store(n + 1, std::memory_order_relaxed);
         return n;
     };
     const long long mean = s.tokens / s.num_seqs;

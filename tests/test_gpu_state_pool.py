@@ -229,6 +229,31 @@ def test_captured_maintenance():
             assert torch.equal(pool.cpu(), want) and to.tolist() == map_ and n.item() == total
 
 
+def test_offsets_past_32_bits():
+    """Pools of more than 2^31 values: slots at both ends."""
+    P, D = 600000, 4096
+    pool = torch.zeros(P, D, device="cuda")
+    pool[P - 1], pool[P - 2] = 3.0, 4.0
+    state_copy(pool, i32([P - 1, P - 2, -1]), i32([0, P - 1, P - 2]))
+    assert (pool[0] == 3).all() and (pool[P - 1] == 4).all() and (pool[P - 2] == 0).all()
+    x = torch.ones(2, D, device="cuda")
+    out = gated_scan_step(x, torch.zeros_like(x), pool, slots=i32([P - 1, 1]))
+    assert (out[0] == 5).all() and (pool[P - 1] == 5).all() and (out[1] == 1).all() and (pool[1] == 1).all()
+    live = torch.zeros(P, dtype=torch.bool, device="cuda")
+    live[[0, P - 1]] = True
+    new_slot, count = state_compact(pool, live)
+    assert count.item() == 2 and new_slot[P - 1].item() == 1 and (pool[1] == 5).all() and (pool[0] == 3).all()
+    del pool, x, out
+    P, H, d = 33000, 16, 64
+    pool = torch.zeros(P, H, d, d, device="cuda")
+    pool[P - 1] = torch.randn(H, d, d, generator=torch.Generator().manual_seed(2)).cuda()
+    state = pool[P - 1:].clone()
+    args = decode_inputs(1, H, d, torch.bfloat16, {})
+    out = decode_step(*args, 0.125, pool, slots=i32([P - 1]))
+    dense = decode_step(*args, 0.125, state)
+    assert torch.equal(out, dense) and torch.equal(pool[P - 1:], state) and not pool[:P - 1].any()
+
+
 def test_on_another_stream():
     pool = pool_of(1, 64, 40000)
     dev, side = pool.cuda(), torch.cuda.Stream()
