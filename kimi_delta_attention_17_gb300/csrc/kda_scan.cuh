@@ -474,6 +474,16 @@ cudaError_t launch_scan_step(const ScanStepArgs &s, cudaStream_t stream);
 // forward: 140 us with a CTA each, 49 so).
 enum ScanOrder { kOrderPlain, kOrderLongest };
 
+// Dynamic shared memory of a scan's CTA: what it needs, and at least as much as
+// keeps one CTA more than S::per_sm off an SM.
+template <typename S>
+constexpr size_t scan_smem(int ranks) {
+    constexpr size_t sm = 228 * 1024, reserved = 1024;  // of an SM; of each CTA beside its own
+    constexpr size_t least = sm / (S::per_sm + 1) - sizeof(typename S::Shared) - reserved + 16;
+    const size_t need = S::smem + ClusterMaps<S::ch>::bytes(ranks);
+    return need > least ? need : least;
+}
+
 // How many clusters of each size of one kernel run at the same time on a device,
 // looked up on first use.
 struct ScanFits {
@@ -503,13 +513,13 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     const int blocks = (s.D + S::ch - 1) / S::ch;
     if (!s.cu && s.num_seqs > 1 && s.T_fixed <= S::tile / S::warps) {
         const long long grid = (long long)((s.num_seqs + S::warps - 1) / S::warps) * blocks;
-        err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::smem);
+        err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem<S>(1));
         if (err != cudaSuccess) return err;
-        kNarrow<<<(unsigned)grid, S::threads, S::smem, stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
+        kNarrow<<<(unsigned)grid, S::threads, scan_smem<S>(1), stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
         return cudaGetLastError();
     }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)(S::smem + ClusterMaps<S::ch>::bytes(kScanMaxRanks)));
+                               (int)scan_smem<S>(kScanMaxRanks));
     if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (err != cudaSuccess) return err;
     const int order = s.cu && s.num_seqs > 1 && s.num_seqs <= kOrderedMost ? kOrderLongest : kOrderPlain;
@@ -525,7 +535,7 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     auto shape = [&](int ranks) {
         attr[0].val.clusterDim.x = ranks;
         cfg.gridDim = dim3((unsigned)(units * ranks));
-        cfg.dynamicSmemBytes = S::smem + ClusterMaps<S::ch>::bytes(ranks);
+        cfg.dynamicSmemBytes = scan_smem<S>(ranks);
     };
     auto fit = [&](int ranks) {  // clusters of this size at the same time
         int n = fits.clusters[dev][ranks].load(std::memory_order_relaxed) - 1;

@@ -12,9 +12,9 @@
 // come in and dx and dg go out once each.
 //
 // The gates' slopes are formed after the exchange, from a and 1 - a kept in
-// registers. Bound by HBM with fp32 gates (131072 x 2048, bf16 x: 571 us, 6.6
-// TB/s); with bf16 gates by latency at 11 % of the warps resident (578 us, 4.6
-// TB/s; 8 x 4096 x 2048 with the norm write 137 us, 4.9 TB/s).
+// registers. Bound by HBM with fp32 gates (131072 x 2048, bf16 x: 573 us, 6.6
+// TB/s); with bf16 gates by latency at 16 % of the warps resident (517 us, 5.2
+// TB/s; 8 x 4096 x 2048 with the norm write 136 us, 4.9 TB/s).
 #include "kda_scan.cuh"
 
 namespace kda {
@@ -30,8 +30,10 @@ struct BwdShape {
     using XS = Slots<XT, vec, tpt, threads>;
     using GS = Slots<GT, vec, tpt, threads>;
     struct Shared {
-        // A, H, U of each group's tokens; then the state and the gradient entering them.
-        float map[Tiling::groups][3][ch];
+        // A and H of each group's tokens, then U in A's place; then the gradient and the
+        // state entering them. (A third row costs clusters of 12 the third CTA per
+        // SM: 131072 x 2048, bf16 gates, 572 us for 517.)
+        float map[Tiling::groups][2][ch];
         L warp_map[2][warps][3][32];  // A, H, U of each warp's tokens
     };
     static constexpr int stages = 2;
@@ -135,7 +137,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
         constexpr bool kKeepC = kGate == KDA_GATE_LOGSIGMOID || kWrite != KDA_WRITE_PLAIN;
         F2 a[kTpt][kPairs], b[kTpt][kPairs], c1[kKeepC ? kTpt : 1][kPairs];
         {
-            Pairs<V> A, H = {}, U = {};
+            Pairs<V> A, H = {};
             Decay<kGate> decay[kPairs];
 #pragma unroll
             for (int j = 0; j < kTpt; ++j) {
@@ -151,33 +153,39 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
                 }
             }
 #pragma unroll
-            for (int j = kTpt - 1; j >= 0; --j) {
-                const Pairs<V> dv = XS::get(ds, st, j);
-#pragma unroll
-                for (int c = 0; c < kPairs; ++c) U[c] = mul2(a[j][c], add2(dv[c], U[c]));
-            }
-#pragma unroll
             for (int c = 0; c < kPairs; ++c) A[c] = decay[c].value();
             store_pairs<V>(&sh.map[group][0][col], A);
             store_pairs<V>(&sh.map[group][1][col], H);
-            store_pairs<V>(&sh.map[group][2][col], U);
         }
         __syncwarp();
         auto entry = [&](int v, int k) -> L & {
             return *reinterpret_cast<L *>(&sh.map[warp * kWarpGroups + v][k][lane * kLaneCh]);
         };
         L A[kWarpGroups], H[kWarpGroups], U[kWarpGroups];
+#pragma unroll
+        for (int v = 0; v < kWarpGroups; ++v) {
+            A[v] = entry(v, 0);
+            H[v] = entry(v, 1);
+        }
+        {
+            Pairs<V> back = {};
+#pragma unroll
+            for (int j = kTpt - 1; j >= 0; --j) {
+                const Pairs<V> dv = XS::get(ds, st, j);
+#pragma unroll
+                for (int c = 0; c < kPairs; ++c) back[c] = mul2(a[j][c], add2(dv[c], back[c]));
+            }
+            __syncwarp();  // every lane has its A
+            store_pairs<V>(&sh.map[group][0][col], back);
+        }
+        __syncwarp();
         {
             L PA, PH, QU;
             lane_set(PA, 1.f);
             lane_set(PH, 0.f);
             lane_set(QU, 0.f);
 #pragma unroll
-            for (int v = 0; v < kWarpGroups; ++v) {
-                A[v] = entry(v, 0);
-                H[v] = entry(v, 1);
-                U[v] = entry(v, 2);
-            }
+            for (int v = 0; v < kWarpGroups; ++v) U[v] = entry(v, 0);
 #pragma unroll
             for (int v = 0; v < kWarpGroups; ++v) {
                 PH = lane_fma(A[v], PH, H[v]);
@@ -232,12 +240,12 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
             }
 #pragma unroll
             for (int v = kWarpGroups - 1; v >= 0; --v) {
-                entry(v, 2) = mine;
+                entry(v, 0) = mine;
                 mine = lane_fma(A[v], mine, U[v]);
             }
         }
         __syncwarp();
-        Pairs<V> h = load_pairs<V>(&sh.map[group][1][col]), e = load_pairs<V>(&sh.map[group][2][col]);
+        Pairs<V> h = load_pairs<V>(&sh.map[group][1][col]), e = load_pairs<V>(&sh.map[group][0][col]);
 #pragma unroll
         for (int j = 0; j < kTpt; ++j)
 #pragma unroll
