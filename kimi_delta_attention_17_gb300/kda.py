@@ -3,6 +3,7 @@ torch CUDA tensors. It only marshals arguments (pointers, sizes, the current
 stream) and allocates outputs and scratch with torch when the caller does not
 pass them; every step of the computation runs in the library's kernels."""
 import ctypes
+import functools
 
 import torch
 
@@ -162,18 +163,21 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on_stream(call, tensors, stream, *args):
-    """call(*args) where allocations and launches belong to the tensors' device and
-    to ``stream`` (the device's current one when None). ``tensors``: name ->
-    tensor or None, the first one not None."""
-    index = -1
-    for name, t in tensors.items():
-        if t is not None:
-            i = t.get_device()
-            if index < 0:
-                index = i
-            elif i != index:
-                raise ValueError("%s must be on the same device as the other tensors" % name)
+@functools.lru_cache(maxsize=None)
+def _one_device():
+    return torch.cuda.device_count() == 1
+
+
+def _on_stream(call, names, tensors, stream, *args):
+    """call(*args, stream handle) where allocations and launches belong to the
+    device of ``tensors`` (called ``names``; some None, the first one not) and to
+    ``stream`` (the device's current one when None)."""
+    if stream is None and _one_device():
+        return call(*args, _raw_stream(0))
+    index = tensors[0].get_device()
+    for name, t in zip(names, tensors):
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s must be on the same device as the other tensors" % name)
     if stream is None:
         if index == torch.cuda.current_device():
             return call(*args, _raw_stream(index))
@@ -242,10 +246,8 @@ def _decode_step_slots(q, k, v, g, beta, scale, state, slots, out, stream, opts,
         _need(out, "out", q.dtype, 3)
         if out.shape != v.shape:
             raise ValueError("out must have v's shape")
-    return _on_stream(_launch_decode_slots,
-                      {"q": q, "k": k, "v": v, "g": g if decay != "none" else None, "beta": beta,
-                       "state": state, "slots": slots, "out": out},
-                      stream, q, k, v, g, beta, scale, state, slots, out, opts)
+    return _on_stream(_launch_decode_slots, ("q", "k", "v", "g", "beta", "state", "slots", "out"),
+                      (q, k, v, g if decay != "none" else None, beta, state, slots, out), stream, q, k, v, g, beta, scale, state, slots, out, opts)
 
 
 def _launch_decode_slots(q, k, v, g, beta, scale, state, slots, out, opts, stream):

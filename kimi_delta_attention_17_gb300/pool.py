@@ -48,8 +48,8 @@ def state_copy(pool, src, dst, *, source=None, slot_dim=0, stream=None):
             raise ValueError("source must have the pool's layers and slot shape")
         if source.data_ptr() == pool.data_ptr() and source_slots == slots:
             source = None
-    _on_stream(_launch_copy, {"pool": pool, "src": src, "dst": dst, "source": source}, stream, pool,
-               src, dst, source, source_slots, slots, layers, nbytes)
+    _on_stream(_launch_copy, ("pool", "src", "dst", "source"), (pool, src, dst, source), stream,
+               pool, src, dst, source, source_slots, slots, layers, nbytes)
     return pool
 
 
@@ -78,9 +78,9 @@ def state_compact(pool, live, *, slot_dim=0, new_slot=None, count=None, stream=N
             _need(t, name, torch.int32, 1)
             if t.shape[0] != n:
                 raise ValueError("%s must be int32 [%d]" % (name, n))
-    return _on_stream(_launch_compact,
-                      {"pool": pool, "live": live, "new_slot": new_slot, "count": count}, stream, pool,
-                      live, new_slot, count, slots, layers, nbytes)
+    return _on_stream(_launch_compact, ("pool", "live", "new_slot", "count"),
+                      (pool, live, new_slot, count), stream,
+                      pool, live, new_slot, count, slots, layers, nbytes)
 
 
 def _launch_compact(pool, live, new_slot, count, slots, layers, nbytes, stream):

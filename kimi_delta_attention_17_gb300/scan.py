@@ -100,9 +100,9 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
     if carries is not None:
         _carries(carries, B, T, N, D)
     return _on_stream(_launch_fwd,
-                      {"x": x, "g": g, "init_state": init_state, "cu_seqlens": cu_seqlens, "out": out,
-                       "final_state": final_state, "carries": carries},
-                      stream, x, g, init_state, cu_seqlens, out, final_state, carries, save_carries,
+                      ("x", "g", "init_state", "cu_seqlens", "out", "final_state", "carries"),
+                      (x, g, init_state, cu_seqlens, out, final_state, carries), stream,
+                      x, g, init_state, cu_seqlens, out, final_state, carries, save_carries,
                       output_final_state, B, T, D, N, opts)
 
 
@@ -141,9 +141,10 @@ def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, d
     if dg is not None:
         _like(dg, "dg", g, "g")
     return _on_stream(_launch_bwd,
-                      {"x": x, "g": g, "dout": dout, "carries": carries, "cu_seqlens": cu_seqlens,
-                       "dfinal_state": dfinal_state, "dinit_state": dinit_state, "dx": dx, "dg": dg},
-                      stream, dout, x, g, carries, cu_seqlens, dfinal_state, dx, dg, dinit_state,
+                      ("x", "g", "dout", "carries", "cu_seqlens", "dfinal_state", "dinit_state", "dx",
+                       "dg"),
+                      (x, g, dout, carries, cu_seqlens, dfinal_state, dinit_state, dx, dg), stream,
+                      dout, x, g, carries, cu_seqlens, dfinal_state, dx, dg, dinit_state,
                       output_dinit_state, B, T, D, N, opts)
 
 
@@ -186,7 +187,7 @@ def gated_scan_step(x, g, state, *, slots=None, out=None, stream=None, gate="log
             raise ValueError("slots must have one entry per row")
     if out is not None:
         _like(out, "out", x, "x")
-    return _on_stream(_launch_step, {"x": x, "g": g, "state": state, "slots": slots, "out": out}, stream,
+    return _on_stream(_launch_step, ("x", "g", "state", "slots", "out"), (x, g, state, slots, out), stream,
                       x, g, state, slots, out, N, D, opts)
 
 

@@ -269,6 +269,25 @@ def test_repeatable_and_on_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(first, r))
 
 
+def test_calls_at_once_on_two_streams():
+    """Clusters of several calls share the GPU; none waits for another's."""
+    how = dict(gate="logsigmoid", write="norm")
+    data = [cuda(make(1, 6000, 512, "bf16", "logsigmoid", seed=s)) for s in range(2)]
+
+    def both(c, **kw):
+        out, final, carries = gated_scan_fwd(c["x"], c["g"], c["init"], save_carries=True, **how, **kw)
+        return (out, final) + gated_scan_bwd(c["dout"], c["x"], c["g"], carries, dfinal_state=c["dfinal"], **how, **kw)
+
+    alone = [both(c) for c in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in data]
+    for _ in range(5):
+        got = [both(c, stream=s) for c, s in zip(data, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_channel_dimensions():
     c = cuda(make(2, 50, 24, "bf16"))
     flat, final, _ = gated_scan_fwd(c["x"], c["g"], c["init"])

@@ -19,6 +19,15 @@ def L():
     return _lib.lib()
 
 
+def test_constants_of_the_header():
+    text = open(_lib.HEADER).read()
+    for name, value in (("KDA_SCAN_CARRY_TOKENS", _lib.SCAN_CARRY_TOKENS),
+                        ("KDA_STATE_COPY_MAX", _lib.STATE_COPY_MAX)):
+        assert "#define %s %d\n" % (name, value) in text
+    for name, value in _lib.WRITE.items():
+        assert "KDA_WRITE_%s = %d" % (name.upper(), value) in text
+
+
 def opts(gate=0, lower=0.0, write=0):
     return ctypes.byref(_lib.ScanOptions(gate, lower, write))
 
