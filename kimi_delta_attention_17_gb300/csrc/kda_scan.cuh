@@ -43,8 +43,8 @@ __device__ __forceinline__ float max_nan(float x, float y) {  // NaN stays NaN
 }
 constexpr float kLog2E = 1.44269504088896341f;
 
-// Two fp32 values that one instruction takes together (FFMA2 and its kin): the
-// scans are short of issue slots before they are short of anything else.
+// Two fp32 values that one instruction takes together (FFMA2 and its kin): few
+// warps are resident, so a step's time goes with the instructions of its chain.
 struct F2 {
     unsigned long long v;
 };
@@ -494,7 +494,7 @@ struct ScanFits {
 // Launches a scan over the (sequence, channel block) pairs. CTAs per cluster:
 // as many as still let all clusters run at the same time, up to the tiles that
 // the longest sequence can have (bf16 backward of 32 pairs of 16384 tokens:
-// 420 us with 1, 123 with 4, 88 with 8, the most that fit, 126 with 9). Where
+// 420 us with 1, 123 with 4, 88 with 8, 81 with 12, the most that fit). Where
 // not even two do, up to 4 as long as that makes no more than five rounds of
 // CTAs: several rounds of short ones leave the SMs less unevenly loaded than
 // one of long ones (512 pairs of 4096 tokens: 230 us with 2, 193 with 4). For
