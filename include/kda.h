@@ -472,12 +472,16 @@ typedef enum {
 
 /*
  * Options of the gated scan. A NULL pointer means {KDA_GATE_LOG, 0,
- * KDA_WRITE_PLAIN}. gate_lower as in kda_options (KDA_GATE_BOUNDED only).
+ * KDA_WRITE_PLAIN, 0}. gate_lower as in kda_options (KDA_GATE_BOUNDED only).
+ * zero_outside: with cu_seqlens, rows of `out`, or of `dx` and `dg`, that no
+ * sequence covers (a packed batch padded to a fixed length) are set to zero if
+ * it is not 0, and left as they were if it is 0.
  */
 typedef struct {
     kda_gate gate;
     float gate_lower;
     kda_write write;
+    int zero_outside;
 } kda_scan_options;
 
 /* Tokens between the states that kda_gated_scan_fwd saves for the backward pass. */
@@ -497,8 +501,10 @@ size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs);
  *  init_state [num_seqs][D] fp32, or NULL for zero initial states
  *  cu_seqlens int32 [num_seqs + 1] device array or NULL, as kda_chunk_fwd.
  *             Its contents are not read on the host; each offset is clamped to
- *             [0, T] before use. Rows outside every sequence are left as they
- *             were.
+ *             [0, T] before use. Unlike kda_chunk_fwd's, they need not begin at
+ *             0 nor end at T: rows before the first offset and from the last
+ *             one on are in no sequence (kda_scan_options.zero_outside).
+ *             Offsets that fall or lie outside [0, T] give unspecified values.
  *  out        [tokens][D], dtype        h_t (written)
  *  final_state[num_seqs][D] fp32 (written), or NULL. May alias init_state
  *             exactly. A zero-length sequence's is its initial state.
@@ -533,8 +539,8 @@ kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_st
  *  dout       [tokens][D], dtype       gradient of out
  *  dfinal_state [num_seqs][D] fp32, or NULL for zero
  *  x, g, carries, cu_seqlens, sizes and options: those of the forward call
- *  dx         [tokens][D], dtype (written)
- *  dg         [tokens][D], g_dtype (written)
+ *  dx         [tokens][D], dtype (written; rows in no sequence: zero_outside)
+ *  dg         [tokens][D], g_dtype (likewise)
  *  dinit_state [num_seqs][D] fp32 (written), or NULL. May alias dfinal_state
  *             exactly. A zero-length sequence's is its dfinal_state (or zero).
  * With KDA_WRITE_NORM the slope of w at a = 1 (log a = 0) is unbounded; where

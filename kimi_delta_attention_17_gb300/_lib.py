@@ -29,7 +29,8 @@ class Options(ctypes.Structure):
 
 class ScanOptions(ctypes.Structure):
     """kda_scan_options of include/kda.h."""
-    _fields_ = [("gate", ctypes.c_int), ("gate_lower", ctypes.c_float), ("write", ctypes.c_int)]
+    _fields_ = [("gate", ctypes.c_int), ("gate_lower", ctypes.c_float), ("write", ctypes.c_int),
+                ("zero_outside", ctypes.c_int)]
 
 
 _vp = ctypes.c_void_p

@@ -449,6 +449,7 @@ kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options
     if (B <= 0 || T < 0 || s->D <= 0 || s->num_seqs <= 0) return KDA_ERR_INVALID_ARGUMENT;
     if (s->cu ? B != 1 : s->num_seqs != B) return KDA_ERR_INVALID_ARGUMENT;
     s->tokens = (long long)B * T;
+    s->zero_outside = s->cu && options && options->zero_outside;
     s->T_fixed = T;
     if (s->tokens >= (1LL << 31) - kChunk) return KDA_ERR_INVALID_ARGUMENT;
     if (s->tokens * s->D >= (1LL << 40)) return KDA_ERR_INVALID_ARGUMENT;

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kScanThreads, FwdShape<XT, GT, kTokens>::per_s
 scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
          const int32_t *__restrict__ cu, XT *__restrict__ out, float *final_state,
          float *__restrict__ carries, int T_fixed, long long tokens, int D, int blocks, int ranks,
-         int num_seqs, int order, float lower) {
+         int num_seqs, int order, bool zero_outside, float lower) {
     using S = FwdShape<XT, GT, kTokens>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -126,6 +126,9 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
 
 #pragma unroll
     for (int i = 0; i < S::stages; ++i) prefetch(i, left - i * less, at + i * stride);
+    if (!kNarrow && zero_outside && has_ch)
+        rows_outside(cu, num_seqs, tokens, (long long)(unit / (unsigned)blocks) * ranks + rank, (long long)num_seqs * ranks,
+                     [&](size_t row) { store_pairs<V>(out + row * D + ch0 + col, Pairs<V>{}); });
     for (int i = 0; i < steps; ++i, at += stride, left -= less) {
         async_wait<S::stages - 1>();
         const int st = i % S::stages;

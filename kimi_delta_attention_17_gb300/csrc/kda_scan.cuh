@@ -434,6 +434,20 @@ __device__ __forceinline__ int kth_longest(const int32_t *cu, int num_seqs, int 
     return n;
 }
 
+// zero(row) for the rows that no packed sequence covers, those before the first
+// offset and from the last one on, shared out over the CTAs of a channel block
+// (this one is number `place` of `places`) and a CTA's groups.
+template <typename F>
+__device__ __forceinline__ void rows_outside(const int32_t *cu, int num_seqs, long long tokens, long long place,
+                                             long long places, F zero) {
+    constexpr int kGroups = kScanThreads / kScanLanes;
+    const long long first = min(max((long long)cu[0], 0LL), tokens);
+    const long long last = min(max((long long)cu[num_seqs], first), tokens);
+    const long long rows = first + tokens - last;
+    for (long long k = place * kGroups + threadIdx.x / kScanLanes; k < rows; k += places * kGroups)
+        zero((size_t)(k < first ? k : k - first + last));
+}
+
 // Row of `carries` that holds the state entering token
 // KDA_SCAN_CARRY_TOKENS * i of the sequence.
 __device__ __forceinline__ long long carry_row(long long begin, int n, long long i) {
@@ -447,6 +461,7 @@ struct ScanArgs {
     const int32_t *cu;
     void *out, *dx, *dg;
     float *final_state, *dinit, *carries;
+    bool zero_outside;  // kda_scan_options, with cu only
     int T_fixed;  // tokens per sequence without cu
     long long tokens;
     int D, num_seqs;
@@ -515,7 +530,8 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
         const long long grid = (long long)((s.num_seqs + S::warps - 1) / S::warps) * blocks;
         err = cudaFuncSetAttribute(kNarrow, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)scan_smem<S>(1));
         if (err != cudaSuccess) return err;
-        kNarrow<<<(unsigned)grid, S::threads, scan_smem<S>(1), stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, s.gate.lower);
+        kNarrow<<<(unsigned)grid, S::threads, scan_smem<S>(1), stream>>>(args..., blocks, 1, s.num_seqs, kOrderPlain, false,
+                                                                 s.gate.lower);
         return cudaGetLastError();
     }
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -560,7 +576,7 @@ cudaError_t launch_scan(const ScanArgs &s, cudaStream_t stream, A... args) {
     }
     if (err != cudaSuccess) return err;
     shape(ranks);
-    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, s.num_seqs, order, s.gate.lower);
+    return cudaLaunchKernelEx(&cfg, kernel, args..., blocks, ranks, s.num_seqs, order, s.zero_outside, s.gate.lower);
 }
 
 // fn<storage type, gate type, gate, write>(args, stream) for a checked call.

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(BwdShape<XT, GT>::threads, BwdShape<XT, GT>::p
 scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict__ x,
          const GT *__restrict__ g, const float *__restrict__ carries, const int32_t *__restrict__ cu,
          XT *__restrict__ dx, GT *__restrict__ dg, float *dinit, int T_fixed, long long tokens, int D,
-         int blocks, int ranks, int num_seqs, int order, float lower) {
+         int blocks, int ranks, int num_seqs, int order, bool zero_outside, float lower) {
     using S = BwdShape<XT, GT>;
     using L = typename S::L;
     using XS = typename S::XS;
@@ -123,6 +123,12 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     };
 
     prefetch(steps - 1, left, at);
+    if (!kNarrow && zero_outside && has_ch)
+        rows_outside(cu, num_seqs, tokens, (long long)(unit / (unsigned)blocks) * ranks + rank, (long long)num_seqs * ranks,
+                     [&](size_t row) {
+                         store_pairs<V>(dx + row * D + ch0 + col, Pairs<V>{});
+                         store_pairs<V>(dg + row * D + ch0 + col, Pairs<V>{});
+                     });
     for (int i = steps - 1; i >= 0; --i, at -= stride, left += more) {
         const int st = i & 1, p = i & 1;
         const long long tile = ((long long)i * ranks + rank) * kTile;  // the CTA's first token

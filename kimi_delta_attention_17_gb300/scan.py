@@ -11,12 +11,13 @@ from .kda import _DTYPES, _need, _on_stream, _ptr
 
 
 @functools.lru_cache(maxsize=64)
-def _scan_options(gate, gate_lower, write):
+def _scan_options(gate, gate_lower, write, zero_outside=False):
     """kda_scan_options by reference, one for each combination in use."""
     if gate not in _lib.GATE or write not in _lib.WRITE:
         raise ValueError("gate must be one of %s and write one of %s"
                          % (sorted(_lib.GATE), sorted(_lib.WRITE)))
-    return ctypes.byref(_lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write]))
+    return ctypes.byref(_lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write],
+                                         zero_outside))
 
 
 def _rows(x, g, lead):
@@ -88,9 +89,10 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
     (w = 1 - a) or "norm" (w = sqrt(1 - a^2)).
     ``save_carries`` (or a ``carries`` buffer) keeps what gated_scan_bwd needs:
     the fp32 state entering every 64th token, [B T // 64 + N, D].
-    Rows of ``out`` outside every sequence are left as they were."""
+    Rows outside every sequence (before cu_seqlens[0], from cu_seqlens[N] on) are
+    zeros in the returned ``out``, and left as they were in one that is given."""
     B, T, D, N = _tokens(x, g, cu_seqlens)
-    opts = _scan_options(gate, gate_lower, write)
+    opts = _scan_options(gate, gate_lower, write, cu_seqlens is not None and out is None)
     if init_state is not None:
         _states(init_state, "init_state", N, x)
     if final_state is not None:
@@ -128,9 +130,11 @@ def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, d
     """The gradient of gated_scan_fwd (kda_gated_scan_bwd): dout of x's shape and
     type, dfinal_state [N, channels...] fp32 or None; x, g, cu_seqlens and the
     options of the forward call, and the ``carries`` that it saved.
-    Returns (dx, dg, dinit_state or None), in the types of x, g and fp32."""
+    Returns (dx, dg, dinit_state or None), in the types of x, g and fp32. Rows
+    outside every sequence have the gradient zero; in a ``dx`` or ``dg`` that is
+    given they are left as they were."""
     B, T, D, N = _tokens(x, g, cu_seqlens)
-    opts = _scan_options(gate, gate_lower, write)
+    opts = _scan_options(gate, gate_lower, write, cu_seqlens is not None and dx is None and dg is None)
     _like(dout, "dout", x, "x")
     _carries(carries, B, T, N, D)
     for t, name in ((dfinal_state, "dfinal_state"), (dinit_state, "dinit_state")):
@@ -150,10 +154,13 @@ def gated_scan_bwd(dout, x, g, carries, cu_seqlens=None, *, dfinal_state=None, d
 
 def _launch_bwd(dout, x, g, carries, cu_seqlens, dfinal_state, dx, dg, dinit_state,
                 output_dinit_state, B, T, D, N, opts, stream):
+    # The option zeroes rows in both or in neither; a fresh one beside a given one is
+    # zeroed whole.
+    fresh = torch.empty_like if cu_seqlens is None or (dx is None and dg is None) else torch.zeros_like
     if dx is None:
-        dx = torch.empty_like(x)
+        dx = fresh(x)
     if dg is None:
-        dg = torch.empty_like(g)
+        dg = fresh(g)
     if dinit_state is None and output_dinit_state:
         dinit_state = torch.empty((N,) + x.shape[2:], dtype=torch.float32, device=x.device)
     status = _lib.lib().kda_gated_scan_bwd(
