@@ -27,6 +27,7 @@ __device__ __forceinline__ void async16(void *smem, const void *gmem) {
 // which move: 61-64 us, 5.4 TB/s; columns of 256 bytes there, and 512 change
 // little: 63) and by some 5 us of lists and first loads on small ones.
 constexpr size_t copy_list_bytes(int n) { return ((size_t)n * 8 + 127) / 128 * 128; }
+constexpr int kFewEntries = 1024;  // launch_state_copy
 constexpr int copy_hash_size(int n) {
     int h = 64;
     while (h < 2 * n) h *= 2;
@@ -305,20 +306,25 @@ cudaError_t launch_state_copy(const void *source, int source_slots, void *pool, 
     int sms = 0;
     cudaError_t err = sm_count(&sms);
     if (err != cudaSuccess) return err;
-    // Two CTAs per SM; beyond 1024 entries a column of one piece each, and the
-    // list, need an SM's whole shared memory for one.
+    // Two CTAs per SM; beyond kFewEntries entries a column of one piece each, and
+    // the list, need an SM's whole shared memory for one. The limit on a kernel's
+    // shared memory is the kernel's, not the launch's, so every call sets the same:
+    // what its most entries need. A smaller one could come between another host
+    // thread's limit and its launch, which would then be refused.
     const size_t lists = copy_list_bytes(n);
-    auto launch = [&](auto kernel, int items, int per_sm) {
-        const size_t smem = lists + 2 * (size_t)items * kPoolThreads * 16;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto launch = [&](auto kernel, int items, int per_sm, int most) {
+        const size_t buffers = 2 * (size_t)items * kPoolThreads * 16;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(copy_list_bytes(most) + buffers));
         if (e != cudaSuccess) return e;
-        kernel<<<sms * per_sm, kPoolThreads, smem, stream>>>(
+        kernel<<<sms * per_sm, kPoolThreads, lists + buffers, stream>>>(
             static_cast<const uint4 *>(source ? source : pool), source ? source_slots : num_slots,
             static_cast<uint4 *>(pool), num_slots, src, dst, n, copy_hash_size(n), layers, (uint32_t)(slot_bytes / 16),
             (int)lists);
         return cudaGetLastError();
     };
-    return n > 1024 ? launch(state_copy_kernel<22>, 22, 1) : launch(state_copy_kernel<12>, 12, 2);
+    return n > kFewEntries ? launch(state_copy_kernel<22>, 22, 1, KDA_STATE_COPY_MAX)
+                           : launch(state_copy_kernel<12>, 12, 2, kFewEntries);
 }
 
 size_t compact_workspace(int num_slots) {
