@@ -10,14 +10,19 @@ from . import _lib
 from .kda import _DTYPES, _need, _on_stream, _ptr
 
 
-@functools.lru_cache(maxsize=64)
 def _scan_options(gate, gate_lower, write, zero_outside=False):
-    """kda_scan_options by reference, one for each combination in use."""
+    """kda_scan_options by reference. The bound counts as the number it is now: a tensor
+    would be known again by its identity, whatever it holds."""
+    return _options_of(gate, float(gate_lower), write, zero_outside)
+
+
+@functools.lru_cache(maxsize=64)
+def _options_of(gate, gate_lower, write, zero_outside):
+    """The options' struct, one for each combination in use."""
     if gate not in _lib.GATE or write not in _lib.WRITE:
         raise ValueError("gate must be one of %s and write one of %s"
                          % (sorted(_lib.GATE), sorted(_lib.WRITE)))
-    return ctypes.byref(_lib.ScanOptions(_lib.GATE[gate], float(gate_lower), _lib.WRITE[write],
-                                         zero_outside))
+    return ctypes.byref(_lib.ScanOptions(_lib.GATE[gate], gate_lower, _lib.WRITE[write], zero_outside))
 
 
 def _rows(x, g, lead):
