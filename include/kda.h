@@ -559,6 +559,7 @@ kda_status kda_gated_scan_bwd(const void *dout, const float *dfinal_state, const
  *  state      [num_slots][D] fp32
  *  slots      int32 [N] device array, or NULL (then row n's state is slot n
  *             and num_slots must be N); as in kda_decode_step_slots
+ * With N = 0 the call does nothing, whatever the pool's size.
  */
 kda_status kda_gated_scan_step(const void *x, const void *g, float *state, const int32_t *slots,
                                void *out, int N, int num_slots, int D, kda_dtype dtype,

@@ -529,7 +529,9 @@ extern "C" kda_status kda_gated_scan_step(const void *x, const void *g, float *s
     ScanStepArgs s = {x, g, state, slots, out, N, num_slots, D, dtype, g_dtype, ScanGate{}};
     const kda_status st = make_scan_gate(options, dtype, g_dtype, &s.gate);
     if (st != KDA_OK) return st;
-    if (N < 0 || D <= 0 || (slots ? num_slots <= 0 : num_slots != N)) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || D <= 0 || num_slots < 0) return KDA_ERR_INVALID_ARGUMENT;
+    // No rows (whose slots may well be a NULL pointer) fit any pool.
+    if (N > 0 && (slots ? num_slots == 0 : num_slots != N)) return KDA_ERR_INVALID_ARGUMENT;
     if ((long long)N * D >= (1LL << 37)) return KDA_ERR_INVALID_ARGUMENT;  // grid of 512-channel blocks
     if (N > 0 && (!x || !g || !state || !out)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16(x) || !aligned16(g) || !aligned16(state) || !aligned16(out) || !aligned4(slots))

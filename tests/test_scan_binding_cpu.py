@@ -22,3 +22,14 @@ def test_lower_bound_is_read_at_every_call():
     lower.fill_(-2.0)
     assert scan._scan_options("bounded", lower, "plain")._obj.gate_lower == -2.0
     assert scan._scan_options("bounded", -2, "plain")._obj.gate_lower == -2.0
+
+
+def test_a_step_of_no_rows_over_a_pool(L):
+    """An empty slots tensor has a NULL pointer; the pool has its slots all the same."""
+    for slots in (None, FAKE):
+        for dtype in (0, 1):
+            assert L.kda_gated_scan_step(None, None, FAKE, slots, None, 0, 4, 8, dtype, dtype, None, None) == OK
+    assert L.kda_gated_scan_step(None, None, None, None, None, 0, 0, 8, 1, 1, None, None) == OK
+    assert L.kda_gated_scan_step(None, None, FAKE, None, None, 0, -1, 8, 1, 1, None, None) == INVALID
+    # Rows without slots still need a state each.
+    assert L.kda_gated_scan_step(FAKE, FAKE, FAKE, None, FAKE, 1, 4, 8, 1, 1, None, None) == INVALID
