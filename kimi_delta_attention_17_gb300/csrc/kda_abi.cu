@@ -442,18 +442,24 @@ kda_status make_scan_gate(const kda_scan_options *o, kda_dtype dtype, kda_dtype 
     return KDA_OK;
 }
 
+// Sizes of a scan call that its kernels' indices and grid hold.
+bool scan_sizes_ok(int B, int T, int D, int num_seqs) {
+    if (B <= 0 || T < 0 || D <= 0 || num_seqs <= 0) return false;
+    const long long tokens = (long long)B * T, most = (1LL << 31) - kChunk;
+    if (tokens >= most || D >= most || num_seqs >= most) return false;
+    if (tokens * D >= (1LL << 40)) return false;
+    return (long long)num_seqs * ((D + 31) / 32) < (1LL << 31);  // the grid
+}
+
 // The checks that the scan's forward and backward calls share.
 kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options) {
     const kda_status st = make_scan_gate(options, s->dtype, s->g_dtype, &s->gate);
     if (st != KDA_OK) return st;
-    if (B <= 0 || T < 0 || s->D <= 0 || s->num_seqs <= 0) return KDA_ERR_INVALID_ARGUMENT;
+    if (!scan_sizes_ok(B, T, s->D, s->num_seqs)) return KDA_ERR_INVALID_ARGUMENT;
     if (s->cu ? B != 1 : s->num_seqs != B) return KDA_ERR_INVALID_ARGUMENT;
     s->tokens = (long long)B * T;
     s->zero_outside = s->cu && options && options->zero_outside;
     s->T_fixed = T;
-    if (s->tokens >= (1LL << 31) - kChunk) return KDA_ERR_INVALID_ARGUMENT;
-    if (s->tokens * s->D >= (1LL << 40)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)s->num_seqs * ((s->D + 31) / 32) >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;  // the grid
     if (s->tokens > 0 && (!s->x || !s->g)) return KDA_ERR_INVALID_ARGUMENT;
     const void *tensors[] = {s->x,  s->g,  s->dout,        s->init,  s->dfinal, s->out,
                              s->dx, s->dg, s->final_state, s->dinit, s->carries};
@@ -468,8 +474,7 @@ kda_status scan_check(ScanArgs *s, int B, int T, const kda_scan_options *options
 }  // namespace
 
 extern "C" size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs) {
-    if (B <= 0 || T < 0 || D <= 0 || num_seqs <= 0) return 0;
-    if (num_seqs != B && B != 1) return 0;
+    if (!scan_sizes_ok(B, T, D, num_seqs) || (num_seqs != B && B != 1)) return 0;
     return (size_t)((long long)B * T / KDA_SCAN_CARRY_TOKENS + num_seqs) * (size_t)D * sizeof(float);
 }
 

@@ -33,3 +33,15 @@ def test_a_step_of_no_rows_over_a_pool(L):
     assert L.kda_gated_scan_step(None, None, FAKE, None, None, 0, -1, 8, 1, 1, None, None) == INVALID
     # Rows without slots still need a state each.
     assert L.kda_gated_scan_step(FAKE, FAKE, FAKE, None, FAKE, 1, 4, 8, 1, 1, None, None) == INVALID
+
+
+def test_carries_size_of_sizes_that_are_refused(L):
+    f = L.kda_gated_scan_carries_size
+    most = 2 ** 31 - 1
+    for bad in ((most, most, most, most), (1, most, 8, 1), (2 ** 20, 2 ** 12, 8, 2 ** 20), (1, 2 ** 22, 2 ** 18, 1),
+                (1, 0, most, most), (1, 0, 8, most), (1, 0, most - 7, 1)):
+        assert f(*bad) == 0, bad
+        B, T, D, N = bad
+        cu = FAKE if N != B else None
+        assert L.kda_gated_scan_fwd(FAKE, FAKE, None, cu, FAKE, None, None, B, T, D, N, 1, 1, None, None) == INVALID
+    assert f(1, 2 ** 20, 2 ** 19, 1) == (2 ** 14 + 1) * 2 ** 21
