@@ -595,9 +595,12 @@ kda_status kda_state_copy(const void *source, int source_slots, void *pool, int 
                           const int32_t *src, const int32_t *dst, int n, int layers,
                           size_t slot_bytes, cudaStream_t stream);
 
+/* Most slots of a pool that kda_state_compact takes: its lists walk it by 32-bit steps. */
+#define KDA_STATE_COMPACT_MAX (1 << 30)
+
 /*
  * Bytes of device workspace kda_state_compact needs: 0 for up to 4096 slots
- * (and for num_slots <= 0).
+ * (and for num_slots <= 0 or above KDA_STATE_COMPACT_MAX).
  */
 size_t kda_state_compact_workspace_size(int num_slots);
 
@@ -607,7 +610,8 @@ size_t kda_state_compact_workspace_size(int num_slots);
  * live, in every layer, so that slots [0, n) are the live ones (a dense batch
  * for kda_decode_step). No other slot is written: slots from n on keep what
  * they held.
- *  pool       [layers][num_slots][slot_bytes]
+ *  pool       [layers][num_slots][slot_bytes]; num_slots above
+ *             KDA_STATE_COMPACT_MAX return KDA_ERR_UNSUPPORTED
  *  live       uint8 [num_slots], nonzero: live (read only)
  *  new_slot   int32 [num_slots] (written): where each slot's state now is, -1
  *             for a slot that was not live

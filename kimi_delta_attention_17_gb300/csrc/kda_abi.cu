@@ -578,7 +578,7 @@ extern "C" kda_status kda_state_copy(const void *source, int source_slots, void 
 }
 
 extern "C" size_t kda_state_compact_workspace_size(int num_slots) {
-    return num_slots > 0 ? compact_workspace(num_slots) : 0;
+    return num_slots > 0 && num_slots <= KDA_STATE_COMPACT_MAX ? compact_workspace(num_slots) : 0;
 }
 
 extern "C" kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live,
@@ -588,6 +588,7 @@ extern "C" kda_status kda_state_compact(void *pool, int num_slots, const uint8_t
     if (!pool_ok(num_slots, layers, slot_bytes)) return KDA_ERR_INVALID_ARGUMENT;
     if (!pool || !live || !new_slot || !count) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned16(pool) || !aligned4(new_slot) || !aligned4(count)) return KDA_ERR_INVALID_ARGUMENT;
+    if (num_slots > KDA_STATE_COMPACT_MAX) return KDA_ERR_UNSUPPORTED;
     const size_t need = compact_workspace(num_slots);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;

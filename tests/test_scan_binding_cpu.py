@@ -45,3 +45,12 @@ def test_carries_size_of_sizes_that_are_refused(L):
         cu = FAKE if N != B else None
         assert L.kda_gated_scan_fwd(FAKE, FAKE, None, cu, FAKE, None, None, B, T, D, N, 1, 1, None, None) == INVALID
     assert f(1, 2 ** 20, 2 ** 19, 1) == (2 ** 14 + 1) * 2 ** 21
+
+
+def test_compaction_of_more_slots_than_its_indices_hold(L):
+    P = 2 ** 30 + 1
+    assert L.kda_state_compact_workspace_size(P) == 0
+    assert L.kda_state_compact_workspace_size(2 ** 31 - 1) == 0
+    assert L.kda_state_compact_workspace_size(2 ** 30) > 2 ** 33
+    for slots in (P, 2 ** 31 - 1):
+        assert L.kda_state_compact(FAKE, slots, FAKE, FAKE, FAKE, 1, 16, FAKE, 2 ** 40, None) == UNSUPPORTED
