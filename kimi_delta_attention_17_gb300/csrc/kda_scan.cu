@@ -290,7 +290,7 @@ scan_step(const XT *__restrict__ x, const GT *__restrict__ g, float *__restrict_
         const Pairs<V> xv = load_pairs<V>(x + at), zv = load_pairs<V>(g + at);
 #pragma unroll
         for (int c = 0; c < V / 2; ++c) {
-            const Gated q = gate_value<kGate, kWrite>(zv[c], lower);
+            const Gated q = step_value<kGate, kWrite>(zv[c], lower);
             h[c] = fma2(q.a, h[c], written<kWrite>(q.a, q.c, xv[c]));
         }
         store_pairs<V>(sp, h);
