@@ -417,8 +417,11 @@ class DecodeGraph:
     between replays. ``state`` [N, H, dk, dv] fp32 is advanced in place by
     every replay (by all ``steps`` steps). ``out`` [steps, N, H, dv] (allocated
     when None) receives the outputs of every replay. ``options`` as in
-    decode_step. Capturing runs no step on ``state``: one warm-up step runs on
-    a copy, outside the graph."""
+    decode_step; with ``slots`` (int32 [N], refilled like the other inputs and
+    read by every step of a replay) ``state`` is a pool [P, H, dk, dv].
+    Capturing runs no step on ``state``: one warm-up step runs outside the
+    graph, on a copy, or with every row a padded one where ``state`` is a
+    pool, of which no copy is made."""
 
     def __init__(self, q, k, v, g, beta, scale, state, *, out=None, **options):
         if q.dim() != 4 or q.shape[0] < 1:
@@ -428,17 +431,23 @@ class DecodeGraph:
             out = torch.empty(tuple(v.shape), dtype=q.dtype, device=q.device)
         self.out = out
 
-        def step(t, st):
+        def step(t, st, options):
             decode_step(q[t], k[t], v[t], None if g is None else g[t], beta[t], scale, st,
                         out=out[t], **options)
 
-        warm = state.clone()
-        step(0, warm)  # loads the library and checks the arguments outside the capture
+        # Loads the library and checks the arguments outside the capture.
+        slots = options.get("slots")
+        if slots is None:
+            step(0, state.clone(), options)
+        elif isinstance(slots, torch.Tensor) and slots.dtype == torch.int32:
+            step(0, state, {**options, "slots": torch.full_like(slots, -1)})
+        else:
+            step(0, state, options)  # refused
         torch.cuda.current_stream().synchronize()
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
             for t in range(self.steps):
-                step(t, state)
+                step(t, state, options)
 
     def replay(self):
         """Runs the captured steps on the current stream."""
