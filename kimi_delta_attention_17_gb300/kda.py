@@ -430,6 +430,7 @@ class DecodeGraph:
         if out is None:
             out = torch.empty(tuple(v.shape), dtype=q.dtype, device=q.device)
         self.out = out
+        self._reads = (q, k, v, g, beta, state, options.get("slots"))  # the graph has their addresses
 
         def step(t, st, options):
             decode_step(q[t], k[t], v[t], None if g is None else g[t], beta[t], scale, st,

@@ -1,8 +1,11 @@
-"""A graph of decode steps over a pool of states: what it costs to build."""
+"""A graph of decode steps over a pool of states: what it costs to build, and what it keeps."""
+import gc
+import weakref
+
 import pytest
 import torch
 
-from kimi_delta_attention_17_gb300 import DecodeGraph, build
+from kimi_delta_attention_17_gb300 import DecodeGraph, build, decode_step
 from tests.test_gpu_state_pool import decode_inputs, i32
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +36,23 @@ def test_building_makes_no_copy_of_the_pool():
     graph.replay()
     torch.cuda.synchronize()
     assert pool[3].any() and pool[P - 1].any() and not pool[4:P - 1].any()
+
+
+def test_keeps_what_its_steps_read():
+    """Tensors that the caller lets go stay alive with the graph."""
+    N, H, d, P = 2, 2, 64, 5
+    stacked, slots = inputs(N, H, d, 2), i32([4, 1])
+    pool = torch.zeros(P, H, d, d, device="cuda")
+    want = pool.clone()
+    outs = [decode_step(*[t[s] for t in stacked], d ** -0.5, want, slots=slots) for s in range(2)]
+    graph = DecodeGraph(*stacked, d ** -0.5, pool, slots=slots)
+    alive = [weakref.ref(t) for t in stacked + [slots]]
+    del stacked, slots
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(pool, want) and torch.equal(graph.out, torch.stack(outs))
+    del graph
+    gc.collect()
+    assert all(r() is None for r in alive)
