@@ -519,7 +519,9 @@ size_t kda_gated_scan_carries_size(int B, int T, int D, int num_seqs);
  *             16-byte pieces, else KDA_ERR_UNSUPPORTED
  * Pointers 16-byte aligned (cu_seqlens 4-byte). Outputs must not overlap inputs
  * or one another, final_state and init_state excepted. No workspace. States
- * and sums are fp32; the results do not depend on the run (no atomics).
+ * and sums are fp32; the results do not depend on the run (no atomics). CTAs
+ * of a cluster wait for one another with a bound; should a wait ever exceed it,
+ * what would have followed from it is NaN.
  */
 kda_status kda_gated_scan_fwd(const void *x, const void *g, const float *init_state,
                               const int32_t *cu_seqlens, void *out, float *final_state,

@@ -181,7 +181,7 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
             if (kNarrow) {
                 carry = lane_fma(sh.warp_map[i & 1][warp][0][lane], carry, sh.warp_map[i & 1][warp][1][lane]);
             } else if (ranks > 1) {
-                if (warp == 0) {
+                if (warp == 0 && !lost) {
                     L TA, TH;
                     lane_set(TA, 1.f);
                     lane_set(TH, 0.f);
@@ -234,6 +234,7 @@ scan_fwd(const XT *__restrict__ x, const GT *__restrict__ g, const float *init,
     }
     async_wait<0>();
     if (final_state && (kNarrow || warp == 0) && rank == 0 && lane_ch) *reinterpret_cast<L *>(final_state + state_at) = carry;
+    if (!kNarrow) cluster_maps_leave(lost);
 }
 
 template <auto kValue> struct Kernel {

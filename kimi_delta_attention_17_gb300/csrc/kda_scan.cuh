@@ -396,10 +396,22 @@ __device__ __forceinline__ void cluster_maps_send(const ClusterMaps<kCh> &m, int
 }
 // Waits for the maps of step `step`. The wait always ends: the CTAs of a cluster
 // run together and send as many maps. Should it not within its bound, `lost`
-// is set, the call waits for nothing more, and its results become NaN.
+// (one value for the warp) is set: the warp waits for no more maps and its
+// results become NaN. A CTA whose warp 0 has lost sends nothing more either, as a
+// map would go to a buffer that others may still read and arm a barrier whose
+// phase is not over; the others' waits for it then give up in turn.
 template <int kCh>
 __device__ __forceinline__ void cluster_maps_wait(const ClusterMaps<kCh> &m, int step, bool &lost) {
-    if (!lost && !tc::mbar_wait_cluster(&m.bar[step & 1], (uint32_t)(step >> 1) & 1u, 1u << 20)) lost = true;
+    if (!lost)
+        lost = __any_sync(0xffffffffu,
+                          !tc::mbar_wait_cluster(&m.bar[step & 1], (uint32_t)(step >> 1) & 1u, 1u << 20));
+}
+// The last thing that a warp does: one that has lost stays until every other
+// thread of the cluster is here or gone, for maps may still be on their way into
+// this CTA's shared memory. (One that has not has received all there are.) The
+// wait ends, as every wait of the others has a bound.
+__device__ __forceinline__ void cluster_maps_leave(bool lost) {
+    if (lost) asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // A value that is the same in every lane, so that the compiler knows: it then

@@ -204,7 +204,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
         }
         __syncthreads();  // warp_map's halves alternate: the only barrier of a step
         {
-            if (ranks > 1 && warp == 0) {
+            if (ranks > 1 && warp == 0 && !lost) {
                 L TA, TU;
                 lane_set(TA, 1.f);
                 lane_set(TU, 0.f);
@@ -302,6 +302,7 @@ scan_bwd(const XT *__restrict__ dout, const float *dfinal, const XT *__restrict_
     }
     async_wait<0>();
     if (dinit && (kNarrow || warp == 0) && rank == 0 && lane_ch) *reinterpret_cast<L *>(dinit + state_at) = u;
+    if (!kNarrow) cluster_maps_leave(lost);
 }
 
 template <typename XT, typename GT, int kGate, int kWrite>
