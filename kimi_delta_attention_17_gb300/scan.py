@@ -95,7 +95,9 @@ def gated_scan_fwd(x, g, init_state=None, cu_seqlens=None, *, out=None, final_st
     ``save_carries`` (or a ``carries`` buffer) keeps what gated_scan_bwd needs:
     the fp32 state entering every 64th token, [B T // 64 + N, D].
     Rows outside every sequence (before cu_seqlens[0], from cu_seqlens[N] on) are
-    zeros in the returned ``out``, and left as they were in one that is given."""
+    zeros in the returned ``out``, and left as they were in one that is given.
+    No autograd graph is built: the gradient is gated_scan_bwd's, which a
+    torch.autograd.Function of the caller's can call."""
     B, T, D, N = _tokens(x, g, cu_seqlens)
     opts = _scan_options(gate, gate_lower, write, cu_seqlens is not None and out is None)
     if init_state is not None:
