@@ -24,7 +24,7 @@ __device__ __forceinline__ void async16(void *smem, const void *gmem) {
 // Each CTA first reduces the entries to the ones that hold: in range, the last
 // of those that name one destination (a hash table in shared memory), and not
 // a slot onto itself. Bound by HBM on large slots (256 beams of 1 MiB, 75 % of
-// which move: 61-64 us, 5.4 TB/s; columns of 256 bytes there, and 512 change
+// which move: 62-64 us, 5.6-5.8 TB/s; columns of 256 bytes there, and 512 change
 // little: 63) and by some 5 us of lists and first loads on small ones.
 constexpr size_t copy_list_bytes(int n) { return ((size_t)n * 8 + 127) / 128 * 128; }
 constexpr int kFewEntries = 1024;  // launch_state_copy

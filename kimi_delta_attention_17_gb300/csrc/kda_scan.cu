@@ -18,9 +18,9 @@
 //
 // Inputs arrive by asynchronous copies into slots of the thread's own (no
 // barrier), up to two tiles ahead. Bound by HBM where the gates are fp32
-// (131072 x 2048, bf16 x: 345 us, 6.2 TB/s); with bf16 gates the 6 bytes of a
+// (131072 x 2048, bf16 x: 349 us, 6.2 TB/s); with bf16 gates the 6 bytes of a
 // value leave 20 instructions or so for it, and latency shows: 272 us, 5.9 TB/s
-// there, 77 us and 5.2 TB/s on 8 x 4096 x 2048 with the norm write. ncu, 32768
+// there, 78 us and 5.1 TB/s on 8 x 4096 x 2048 with the norm write. ncu, 32768
 // tokens: issue slots 39 % busy with bf16 gates and 37 % with fp32 ones, 11 and
 // 16 % of the warps resident (registers: a and w x of 64 and 32 values a
 // thread); the largest stalls are fixed latency and the copies' arrival.
@@ -269,9 +269,10 @@ cudaError_t launch_fwd(const ScanArgs &s, cudaStream_t stream) {
     return launch(FwdShape<XT, GT>(), Kernel<scan_fwd<XT, GT, kGate, kWrite, kTokens, false>>(), Narrow());
 }
 
-// One step: a thread per 16-byte piece of g, every load issued before the first
-// use. Bound by HBM (2048 rows of 4096 channels out of a pool of twice as many:
-// 22.6 us, 5.9 TB/s) or by the launch.
+// One step: a thread per 16-byte piece of g, all of its loads in flight together
+// (over slots from when the slot's number is there). Bound by HBM (2048 rows of
+// 4096 channels out of a pool of twice as many: 22.6 us, 5.9 TB/s) or by the
+// launch.
 constexpr int kStepThreads = 128;
 template <typename XT, typename GT, int kGate, int kWrite>
 __global__ void __launch_bounds__(kStepThreads)

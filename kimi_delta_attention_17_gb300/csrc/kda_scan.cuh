@@ -286,8 +286,9 @@ __device__ __forceinline__ void store_pairs(float *to, const Pairs<V> &x) {
 // pieces of a row's block of channels, a warp four groups of consecutive
 // tokens, a CTA 16. 32 values a thread, 16 where all of them are fp32 and arrive
 // in twice the bytes (measured, 131072 tokens of 2048 channels, forward: bf16
-// 336 us with 32, 518 with 16 in twice the threads; bf16 with fp32 gates 346 and
-// 381; the 20011 packed fp32 tokens 62 us with 16, 63 with 32).
+// 336 us with 32, 518 with 16 in twice the threads, and as these are few long
+// chains 272 with the 64 that they have now, see few_long_chains; bf16 with fp32
+// gates 346 and 381; the 20011 packed fp32 tokens 62 us with 16, 63 with 32).
 constexpr int kScanThreads = 128;
 constexpr int kScanLanes = 8;                 // threads across the channels
 constexpr int kWarpGroups = 32 / kScanLanes;  // groups per warp

@@ -12,9 +12,9 @@
 // come in and dx and dg go out once each.
 //
 // The gates' slopes are formed after the exchange, from a and 1 - a kept in
-// registers. Bound by HBM with fp32 gates (131072 x 2048, bf16 x: 573 us, 6.6
-// TB/s); with bf16 gates by latency at 16 % of the warps resident (517 us, 5.2
-// TB/s; 8 x 4096 x 2048 with the norm write 136 us, 4.9 TB/s).
+// registers. Bound by HBM with fp32 gates (131072 x 2048, bf16 x: 576 us, 6.5
+// TB/s); with bf16 gates by latency at 16 % of the warps resident (513 us, 5.2
+// TB/s; 8 x 4096 x 2048 with the norm write 133 us, 5.0 TB/s).
 #include "kda_scan.cuh"
 
 namespace kda {
