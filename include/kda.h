@@ -628,6 +628,181 @@ kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live, int
                              size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * One call for up to K tokens of each of N rows: what K calls of
+ * kda_decode_step_slots compute, in one pass over the states (drafts to verify,
+ * accepted tokens to commit, a short continuation). Token t of row n is its
+ * t-th: the tensors have a token dimension after the rows',
+ *  q, k [N][K][H][dk], v, out [N][K][H][dv], g [N][K][H][dk] fp32 (or [N][K][H]
+ *             with KDA_DECAY_SCALAR), beta [N][K][H] fp32
+ *  state      [num_slots][H][dk][dv] fp32
+ *  slots      int32 [N] device array, or NULL (then row n's state is slot n and
+ *             num_slots must be N). As in kda_decode_step_slots: rows out of
+ *             [0, num_slots) touch no state and get zeros; with write_state,
+ *             slots in range must be distinct
+ *  counts     int32 [N] device array, or NULL (K tokens each): row n takes its
+ *             first counts[n] tokens (clamped to [0, K]). Outputs behind them are
+ *             zeros; a row of no tokens leaves its state as it was
+ *  out        written, or NULL where no outputs are wanted
+ *  write_state nonzero: the states after the rows' last tokens are written;
+ *             0: no state is changed. Without outputs it must be nonzero
+ * Results equal the single steps' up to fp32 rounding. No workspace; options
+ * and errors as kda_decode_step_opt.
+ */
+kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const float *g,
+                             const float *beta, float scale, float *state, const int32_t *slots,
+                             const int32_t *counts, void *out, int N, int K, int num_slots, int H,
+                             int dk, int dv, kda_dtype dtype, const kda_options *options,
+                             int write_state, cudaStream_t stream);
+
+/*
+ * Gradient of kda_output_gate_rmsnorm. With r = 1 / sqrt(mean_c o_c^2 + eps),
+ * n = o r and s = sigmoid(z), per token and head,
+ *
+ *     u  = w o dout o s,         d_o = r (u - n mean_c(u_c n_c)),
+ *     dz = u o n o (1 - s),      dweight = sum over tokens and heads of dout o s o n.
+ *
+ *  dout, o, z, d_o, dz [tokens][H][dv], dtype
+ *  weight     [dv] fp32 or NULL, as in the forward call
+ *  dweight    [dv] fp32 (written), or NULL where it is not wanted
+ *  workspace  kda_output_gate_rmsnorm_bwd_workspace_size(...) bytes, 256-byte
+ *             aligned, where dweight is given; contents on entry are ignored
+ * d_o may alias dout, o or z exactly, and dz likewise (not one another). Sums are
+ * fp32 in a fixed order (no atomics). Sizes and alignment as the forward call.
+ */
+size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv);
+kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z,
+                                       const float *weight, float eps, void *d_o, void *dz,
+                                       float *dweight, long long tokens, int H, int dv,
+                                       kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/*
+ * Root-mean-square norm of rows (before a layer's projections), with the
+ * residual's addition in front of it:
+ *
+ *     h = x + residual,   out = w o h / sqrt(mean_c h_c^2 + eps)
+ *
+ *  x          [rows][D], dtype
+ *  residual   [rows][D], residual_dtype, or NULL (h = x)
+ *  weight     [D] fp32 or NULL (ones)
+ *  eps        finite, > 0
+ *  out        [rows][D], dtype (written)
+ *  residual_out [rows][D], residual_dtype (written): h, rounded to that type;
+ *             what is normalised is h as it stands there, so that the backward
+ *             call, which reads it, takes the same values. Given where residual
+ *             is, and may alias it exactly
+ *  rstd       [rows] fp32 (written), or NULL: 1 / sqrt(mean h^2 + eps), for
+ *             kda_rmsnorm_bwd
+ *  dtype, residual_dtype: (BF16, BF16), (BF16, F32) or (F32, F32); (F32, BF16)
+ *             returns KDA_ERR_UNSUPPORTED. residual_dtype is not read without
+ *             a residual
+ *  rows       0 .. 2^31 - 1;  D a multiple of 8, at most 32768, else
+ *             KDA_ERR_UNSUPPORTED
+ * Pointers 16-byte aligned (rstd 4-byte). Outputs must not overlap inputs or one
+ * another, but for residual_out. Sums are fp32. No workspace; one launch.
+ */
+kda_status kda_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps,
+                           void *out, void *residual_out, float *rstd, long long rows, int D,
+                           kda_dtype dtype, kda_dtype residual_dtype, cudaStream_t stream);
+
+/* Values of a row under one scale where kda_rmsnorm_quant has scales in blocks. */
+#define KDA_NORM_SCALE_BLOCK 128
+
+/*
+ * kda_rmsnorm_fwd with its output in 8 bits (e4m3), for a projection in 8 bits:
+ * with y the fp32 output and m the largest magnitude of y in a block,
+ *
+ *     scale = m / 448,   q = e4m3(y * (448 / m)),   y ~ q * scale.
+ *
+ *  q          [rows][D] e4m3 (written)
+ *  scales     [rows][blocks] fp32 (written)
+ *  scale_block 0: one block, the row; KDA_NORM_SCALE_BLOCK: blocks of that many
+ *             values, the last of a row what is left (ceil(D / 128) blocks)
+ * A block with m < 2^-100 is zeros with scale 0; one that holds a NaN has scale
+ * NaN. Other arguments and errors as kda_rmsnorm_fwd (scales 4-byte aligned).
+ */
+kda_status kda_rmsnorm_quant(const void *x, const void *residual, const float *weight, float eps,
+                             void *q, float *scales, void *residual_out, long long rows, int D,
+                             int scale_block, kda_dtype dtype, kda_dtype residual_dtype,
+                             cudaStream_t stream);
+
+/* Bytes of device workspace kda_rmsnorm_bwd needs for dweight. 0 for invalid sizes. */
+size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D);
+
+/*
+ * Gradient of kda_rmsnorm_fwd. With n = h rstd and u = w o dout, per row,
+ *
+ *     dx = dresidual = dh + rstd (u - n mean_c(u_c n_c)),   dweight = sum_rows dout o n.
+ *
+ *  dout       [rows][D], dtype: gradient of out
+ *  h          [rows][D], h_dtype: the forward call's residual_out, or x without
+ *             a residual
+ *  rstd       [rows] fp32, of the forward call
+ *  dh         [rows][D], h_dtype, or NULL for zero: the gradient that reaches
+ *             residual_out from what follows
+ *  dx         [rows][D], dtype (written)
+ *  dresidual  [rows][D], h_dtype (written), or NULL: dx serves for both where
+ *             the types are the same
+ *  dweight    [D] fp32 (written), or NULL where it is not wanted
+ *  workspace  kda_rmsnorm_bwd_workspace_size(rows, D) bytes, 256-byte aligned,
+ *             where dweight is given; contents on entry are ignored
+ * dx may alias dout, and dresidual dh, exactly. Sums are fp32 in a fixed order (no
+ * atomics). Types, sizes and alignment as the forward call.
+ */
+kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd,
+                           const float *weight, const void *dh, void *dx, void *dresidual,
+                           float *dweight, long long rows, int D, kda_dtype dtype,
+                           kda_dtype h_dtype, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* How kda_state_quantize holds a value. */
+typedef enum {
+    KDA_STORE_INT8 = 0, /* whole numbers in [-127, 127], the largest magnitude as 127 */
+    KDA_STORE_E4M3 = 1  /* e4m3, the largest magnitude as 448 */
+} kda_store_format;
+
+/*
+ * States kept in 8 bits (parked requests, the states of shared prefixes): for
+ * i < n and in every layer
+ *
+ *     store[layer][dst[i]] = codes of pool[layer][src[i]]    (of zeros where src[i] < 0)
+ *
+ * with one scale for each block of `block` consecutive values. With m a block's
+ * largest magnitude and top = 127 (INT8) or 448 (E4M3),
+ *
+ *     scale = m * (1 / top),   code = round(x * (top / m)),   value = code * scale,
+ *
+ * to the nearest code, ties to even; top / m and the products are fp32. So a
+ * value is off by at most half a code of INT8, m / 254, or by 2^-4 of itself with
+ * E4M3, its smallest code m / 229376 apart. A block with m < 2^-100 is held as
+ * zeros; one with a value that is not finite comes back as NaN throughout.
+ *  pool       [layers][num_slots][slot_values] fp32
+ *  store      [layers][store_slots][slot_values], one byte each (written)
+ *  scales     [layers][store_slots][slot_values / block] fp32 (written)
+ *  src, dst   int32 [n] device arrays. As in kda_state_copy: entries whose dst is
+ *             out of range, or whose src is not below the source's slots, are
+ *             skipped; of entries that name one destination the last holds
+ *  n          0 .. KDA_STATE_COPY_MAX, else KDA_ERR_UNSUPPORTED
+ *  block      32, 64 or 128; slot_values a positive multiple of it, at most 2^32
+ *  format     kda_store_format
+ * Slots of pool and store 16-byte aligned, scales 4-byte. pool, store and scales
+ * must not overlap. No workspace; one launch.
+ */
+kda_status kda_state_quantize(const float *pool, int num_slots, void *store, float *scales,
+                              int store_slots, const int32_t *src, const int32_t *dst, int n,
+                              int layers, long long slot_values, int block, int format,
+                              cudaStream_t stream);
+
+/*
+ * The way back: pool[layer][dst[i]] = values of store[layer][src[i]] (zeros where
+ * src[i] < 0). Arguments and errors as kda_state_quantize.
+ */
+kda_status kda_state_dequantize(const void *store, const float *scales, int store_slots,
+                                float *pool, int num_slots, const int32_t *src,
+                                const int32_t *dst, int n, int layers, long long slot_values,
+                                int block, int format, cudaStream_t stream);
+
+/*
  * Diagnostic of the failure detection (no counterpart on the pages): launches
  * one CTA that waits, with the kernels' bounded mbarrier wait limited to
  * `limit` polls (1 .. 4194304), on a barrier nothing ever completes; when the

@@ -19,6 +19,8 @@ GATE = {"log": 0, "logsigmoid": 1, "bounded": 2}          # kda_gate
 WRITE = {"plain": 0, "complement": 1, "norm": 2}          # kda_write
 SCAN_CARRY_TOKENS = 64                                    # KDA_SCAN_CARRY_TOKENS
 STATE_COPY_MAX = 4096                                     # KDA_STATE_COPY_MAX
+NORM_SCALE_BLOCK = 128                                    # KDA_NORM_SCALE_BLOCK
+STORE = {"int8": 0, "e4m3": 1}                            # kda_store_format
 
 
 class Options(ctypes.Structure):
@@ -34,6 +36,7 @@ class ScanOptions(ctypes.Structure):
 
 
 _vp = ctypes.c_void_p
+_ll = ctypes.c_longlong
 _SIGNATURES = {
     "kda_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "kda_chunk_fwd_workspace_size": ([ctypes.c_int] * 6 + [ctypes.c_int], ctypes.c_size_t),
@@ -71,6 +74,19 @@ _SIGNATURES = {
     "kda_state_compact_workspace_size": ([ctypes.c_int], ctypes.c_size_t),
     "kda_state_compact": ([_vp, ctypes.c_int, _vp, _vp, _vp, ctypes.c_int, ctypes.c_size_t, _vp,
                            ctypes.c_size_t, _vp], ctypes.c_int),
+    "kda_decode_tokens": ([_vp] * 5 + [ctypes.c_float] + [_vp] * 4 + [ctypes.c_int] * 7 + [_vp, ctypes.c_int, _vp],
+                          ctypes.c_int),
+    "kda_output_gate_rmsnorm_bwd_workspace_size": ([_ll, ctypes.c_int, ctypes.c_int], ctypes.c_size_t),
+    "kda_output_gate_rmsnorm_bwd": ([_vp] * 4 + [ctypes.c_float] + [_vp] * 3 + [_ll] + [ctypes.c_int] * 3
+                                    + [_vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "kda_rmsnorm_fwd": ([_vp] * 3 + [ctypes.c_float] + [_vp] * 3 + [_ll] + [ctypes.c_int] * 3 + [_vp], ctypes.c_int),
+    "kda_rmsnorm_quant": ([_vp] * 3 + [ctypes.c_float] + [_vp] * 3 + [_ll] + [ctypes.c_int] * 4 + [_vp], ctypes.c_int),
+    "kda_rmsnorm_bwd_workspace_size": ([_ll, ctypes.c_int], ctypes.c_size_t),
+    "kda_rmsnorm_bwd": ([_vp] * 8 + [_ll] + [ctypes.c_int] * 3 + [_vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "kda_state_quantize": ([_vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int, _ll,
+                            ctypes.c_int, ctypes.c_int, _vp], ctypes.c_int),
+    "kda_state_dequantize": ([_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, ctypes.c_int, _ll,
+                              ctypes.c_int, ctypes.c_int, _vp], ctypes.c_int),
     "kda_selftest_wait_timeout": ([_vp, ctypes.c_uint, _vp], ctypes.c_int),
     "kda_output_gate_rmsnorm": ([_vp, _vp, _vp, ctypes.c_float, _vp, ctypes.c_longlong,
                                  ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp], ctypes.c_int),

@@ -611,3 +611,201 @@ extern "C" kda_status kda_output_gate_rmsnorm(const void *o, const void *z, cons
         launch_output_gate_rmsnorm(o, z, weight, eps, out, tokens * H, dv, dtype, stream);
     return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
+
+namespace {
+
+// Most values of a row that the row norms keep in a CTA's registers.
+constexpr int kNormMostD = 32768;
+
+bool float_type(kda_dtype t) { return t == KDA_DTYPE_F32 || t == KDA_DTYPE_BF16; }
+
+// Sizes of a row norm that its kernels' indices and grid hold.
+bool norm_sizes_ok(long long rows, int D) { return rows >= 0 && rows < (1LL << 31) && D > 0; }
+kda_status norm_types_ok(int D, kda_dtype dtype, kda_dtype other) {
+    if (D % 8 != 0 || D > kNormMostD) return KDA_ERR_UNSUPPORTED;
+    return dtype == KDA_DTYPE_F32 && other != KDA_DTYPE_F32 ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+// What the norm's two forward calls share.
+kda_status norm_check(const NormArgs &a) {
+    if (!float_type(a.dtype) || (a.residual && !float_type(a.residual_dtype))) return KDA_ERR_INVALID_ARGUMENT;
+    if (!norm_sizes_ok(a.rows, a.D) || !(a.eps > 0.f) || !isfinite(a.eps)) return KDA_ERR_INVALID_ARGUMENT;
+    if (a.rows > 0 && (!a.x || !a.residual != !a.residual_out)) return KDA_ERR_INVALID_ARGUMENT;
+    const void *tensors[] = {a.x, a.residual, a.w, a.out, a.q, a.residual_out};
+    for (const void *p : tensors)
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(a.rstd) || !aligned4(a.scales)) return KDA_ERR_INVALID_ARGUMENT;
+    return norm_types_ok(a.D, a.dtype, a.residual ? a.residual_dtype : KDA_DTYPE_F32);
+}
+
+size_t parts_bytes(long long rows_of_ctas, int most, int D) {
+    return (size_t)(rows_of_ctas < most ? rows_of_ctas : most) * (size_t)D * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" kda_status kda_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps, void *out,
+                                      void *residual_out, float *rstd, long long rows, int D, kda_dtype dtype,
+                                      kda_dtype residual_dtype, cudaStream_t stream) {
+    NormArgs a = {};
+    a.x = x;
+    a.residual = residual;
+    a.w = weight;
+    a.eps = eps;
+    a.out = out;
+    a.residual_out = residual_out;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.D = D;
+    a.dtype = dtype;
+    a.residual_dtype = residual_dtype;
+    const kda_status st = norm_check(a);
+    if (st != KDA_OK) return st;
+    if (rows > 0 && !out) return KDA_ERR_INVALID_ARGUMENT;
+    return launch_rmsnorm(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_rmsnorm_quant(const void *x, const void *residual, const float *weight, float eps, void *q,
+                                        float *scales, void *residual_out, long long rows, int D, int scale_block,
+                                        kda_dtype dtype, kda_dtype residual_dtype, cudaStream_t stream) {
+    NormArgs a = {};
+    a.x = x;
+    a.residual = residual;
+    a.w = weight;
+    a.eps = eps;
+    a.q = q;
+    a.scales = scales;
+    a.scale_block = scale_block;
+    a.residual_out = residual_out;
+    a.rows = rows;
+    a.D = D;
+    a.dtype = dtype;
+    a.residual_dtype = residual_dtype;
+    if (scale_block != 0 && scale_block != KDA_NORM_SCALE_BLOCK) return KDA_ERR_INVALID_ARGUMENT;
+    const kda_status st = norm_check(a);
+    if (st != KDA_OK) return st;
+    if (rows > 0 && (!q || !scales)) return KDA_ERR_INVALID_ARGUMENT;
+    return launch_rmsnorm(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D) {
+    if (!norm_sizes_ok(rows, D) || norm_types_ok(D, KDA_DTYPE_F32, KDA_DTYPE_F32) != KDA_OK) return 0;
+    return parts_bytes(rows, kNormParts, D);
+}
+
+extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd, const float *weight,
+                                      const void *dh, void *dx, void *dresidual, float *dweight, long long rows, int D,
+                                      kda_dtype dtype, kda_dtype h_dtype, void *workspace, size_t workspace_bytes,
+                                      cudaStream_t stream) {
+    if (!float_type(dtype) || !float_type(h_dtype) || !norm_sizes_ok(rows, D)) return KDA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && (!dout || !h || !rstd || !dx)) return KDA_ERR_INVALID_ARGUMENT;
+    const void *tensors[] = {dout, h, weight, dh, dx, dresidual};
+    for (const void *p : tensors)
+        if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(rstd) || !aligned4(dweight)) return KDA_ERR_INVALID_ARGUMENT;
+    const kda_status st = norm_types_ok(D, dtype, h_dtype);
+    if (st != KDA_OK) return st;
+    if (dweight && rows > 0 && (!workspace || workspace_bytes < kda_rmsnorm_bwd_workspace_size(rows, D)))
+        return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
+    const NormBwdArgs a = {dout, h, rstd, weight, dh, dx, dresidual, dweight, static_cast<float *>(workspace), rows, D,
+                           dtype, h_dtype};
+    return launch_rmsnorm_bwd(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv) {
+    if (tokens < 0 || H <= 0 || tokens >= (1LL << 34) / H || (dv != 64 && dv != 128)) return 0;
+    return parts_bytes(tokens * H, kGateParts, dv);
+}
+
+extern "C" kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z, const float *weight,
+                                                  float eps, void *d_o, void *dz, float *dweight, long long tokens, int H,
+                                                  int dv, kda_dtype dtype, void *workspace, size_t workspace_bytes,
+                                                  cudaStream_t stream) {
+    if (!float_type(dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    if (tokens < 0 || H <= 0 || !(eps > 0.f) || !isfinite(eps)) return KDA_ERR_INVALID_ARGUMENT;
+    if (tokens >= (1LL << 34) / H) return KDA_ERR_INVALID_ARGUMENT;
+    if (tokens > 0 && (!dout || !o || !z || !d_o || !dz)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(dout) || !aligned16(o) || !aligned16(z) || !aligned16(d_o) || !aligned16(dz))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(weight) || !aligned4(dweight)) return KDA_ERR_INVALID_ARGUMENT;
+    if (dv != 64 && dv != 128) return KDA_ERR_UNSUPPORTED;
+    if (dweight && tokens > 0 &&
+        (!workspace || workspace_bytes < kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv)))
+        return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
+    const GateBwdArgs a = {dout, o, z, weight, eps, d_o, dz, dweight, static_cast<float *>(workspace), tokens * H, dv, dtype};
+    return launch_output_gate_rmsnorm_bwd(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+namespace {
+
+kda_status store_check(const StoreArgs &a, const void *reads, size_t reads_bytes, const void *writes, size_t writes_bytes,
+                       int format) {
+    if (format != KDA_STORE_INT8 && format != KDA_STORE_E4M3) return KDA_ERR_INVALID_ARGUMENT;
+    if (a.n < 0 || !a.pool || !a.store || !a.scales || (a.n > 0 && (!a.src || !a.dst))) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(a.pool) || !aligned16(a.store) || !aligned4(a.scales) || !aligned4(a.src) || !aligned4(a.dst))
+        return KDA_ERR_INVALID_ARGUMENT;
+    const uintptr_t r = reinterpret_cast<uintptr_t>(reads), w = reinterpret_cast<uintptr_t>(writes);
+    if (r < w + writes_bytes && w < r + reads_bytes) return KDA_ERR_INVALID_ARGUMENT;
+    if (a.n > KDA_STATE_COPY_MAX) return KDA_ERR_UNSUPPORTED;
+    // The grid: a CTA for every 4096 values of every entry.
+    const long long pieces = (a.slot_values + 4095) / 4096;
+    return pieces * a.layers >= (1LL << 31) / KDA_STATE_COPY_MAX && pieces * a.layers * a.n >= (1LL << 31)
+               ? KDA_ERR_UNSUPPORTED
+               : KDA_OK;
+}
+
+bool store_sizes_ok(int num_slots, int store_slots, int layers, long long slot_values, int block) {
+    if (block != 32 && block != 64 && block != 128) return false;
+    if (slot_values <= 0 || slot_values % block != 0 || slot_values > (1LL << 32)) return false;
+    return pool_ok(num_slots, layers, (size_t)slot_values * 4) && pool_ok(store_slots, layers, (size_t)slot_values);
+}
+
+}  // namespace
+
+extern "C" kda_status kda_state_quantize(const float *pool, int num_slots, void *store, float *scales, int store_slots,
+                                         const int32_t *src, const int32_t *dst, int n, int layers, long long slot_values,
+                                         int block, int format, cudaStream_t stream) {
+    if (!store_sizes_ok(num_slots, store_slots, layers, slot_values, block)) return KDA_ERR_INVALID_ARGUMENT;
+    const StoreArgs a = {const_cast<float *>(pool), num_slots, static_cast<uint8_t *>(store), scales, store_slots, src, dst,
+                         n, layers, slot_values, block, format == KDA_STORE_INT8};
+    const size_t values = (size_t)slot_values * layers;
+    const kda_status st = store_check(a, pool, 4 * values * num_slots, store, values * store_slots, format);
+    if (st != KDA_OK) return st;
+    return launch_state_quantize(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_state_dequantize(const void *store, const float *scales, int store_slots, float *pool,
+                                           int num_slots, const int32_t *src, const int32_t *dst, int n, int layers,
+                                           long long slot_values, int block, int format, cudaStream_t stream) {
+    if (!store_sizes_ok(num_slots, store_slots, layers, slot_values, block)) return KDA_ERR_INVALID_ARGUMENT;
+    const StoreArgs a = {pool, num_slots, static_cast<uint8_t *>(const_cast<void *>(store)), const_cast<float *>(scales),
+                         store_slots, src, dst, n, layers, slot_values, block, format == KDA_STORE_INT8};
+    const size_t values = (size_t)slot_values * layers;
+    const kda_status st = store_check(a, store, values * store_slots, pool, 4 * values * num_slots, format);
+    if (st != KDA_OK) return st;
+    return launch_state_dequantize(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                        float scale, float *state, const int32_t *slots, const int32_t *counts, void *out,
+                                        int N, int K, int num_slots, int H, int dk, int dv, kda_dtype dtype,
+                                        const kda_options *options, int write_state, cudaStream_t stream) {
+    TokensArgs a = {q, k, v, g, beta, scale, state, slots, counts, out, N, K, num_slots, H, dk, dtype, Prologue{},
+                    write_state != 0};
+    if (!make_prologue(options, &a.pro)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!float_type(dtype)) return KDA_ERR_INVALID_ARGUMENT;
+    if (N < 0 || K < 0 || H <= 0 || dk <= 0 || dv <= 0 || num_slots < 0 || !isfinite(scale)) return KDA_ERR_INVALID_ARGUMENT;
+    if (N > 0 && (slots ? num_slots == 0 : num_slots != N)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)N * H >= (1LL << 31) || (long long)num_slots * H >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
+    if ((long long)N * H >= (1LL << 46) / (K > 0 ? K : 1) / dk) return KDA_ERR_INVALID_ARGUMENT;
+    const bool some = N > 0 && K > 0;
+    if (some && (!q || !k || !v || !beta || !state || (!out && !write_state))) return KDA_ERR_INVALID_ARGUMENT;
+    if (!g_ok(g, a.pro, some)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out))
+        return KDA_ERR_INVALID_ARGUMENT;
+    if (!aligned4(beta) || !aligned4(slots) || !aligned4(counts)) return KDA_ERR_INVALID_ARGUMENT;
+    if (!dims_ok(dk, dv)) return KDA_ERR_UNSUPPORTED;
+    return launch_decode_tokens(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}

@@ -10,47 +10,13 @@
 // squares by a butterfly within the row's lanes, scale, gate, store). Pure HBM
 // streaming: o and z read once, out written once; the loads in flight per
 // lane are what keep HBM busy.
-#include "kda_internal.cuh"
+#include "kda_rows.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kEpiWarps = 8;   // warps per CTA
 constexpr int kEpiPasses = 4;  // rows in flight per lane
-
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 &r, float *x);
-template <>
-__device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4 &r, float *x) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-}
-template <>
-__device__ __forceinline__ void unpack16<float>(const uint4 &r, float *x) {
-    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float *x);
-template <>
-__device__ __forceinline__ uint4 pack16<__nv_bfloat16>(const float *x) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return make_uint4(u[0], u[1], u[2], u[3]);
-}
-template <>
-__device__ __forceinline__ uint4 pack16<float>(const float *x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-}
 
 template <int D, typename T>
 struct EpiShape {

@@ -181,4 +181,80 @@ cudaError_t launch_state_compact(void *pool, int num_slots, const uint8_t *live,
                                  int32_t *count, int layers, size_t slot_bytes, void *workspace,
                                  cudaStream_t stream);
 
+// Row norm (checked arguments): out in x's type, or q (e4m3) with scales where q is not NULL.
+struct NormArgs {
+    const void *x, *residual;  // residual, residual_out: NULL, or both
+    const float *w;
+    float eps;
+    void *out, *q;
+    float *scales;
+    int scale_block;  // values under one scale, 0: the row
+    void *residual_out;
+    float *rstd;
+    long long rows;
+    int D;
+    kda_dtype dtype, residual_dtype;
+};
+cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream);
+
+// Most CTAs of the norms' gradients, each of which leaves one row of a weight gradient's parts.
+constexpr int kNormParts = 608, kGateParts = 1216;
+
+struct NormBwdArgs {
+    const void *dy, *h;
+    const float *rstd, *w;
+    const void *dh;
+    void *dx, *dres;
+    float *dweight, *part;
+    long long rows;
+    int D;
+    kda_dtype dtype, h_dtype;
+};
+cudaError_t launch_rmsnorm_bwd(const NormBwdArgs &a, cudaStream_t stream);
+
+struct GateBwdArgs {
+    const void *dout, *o, *z;
+    const float *w;
+    float eps;
+    void *d_o, *dz;
+    float *dweight, *part;
+    long long rows;
+    int dv;
+    kda_dtype dtype;
+};
+cudaError_t launch_output_gate_rmsnorm_bwd(const GateBwdArgs &a, cudaStream_t stream);
+
+// Values held in 8 bits: a block (a row) whose largest magnitude is below this is held as zeros.
+constexpr float kStoreTiny = 7.888609052210118e-31f;  // 2^-100
+
+struct StoreArgs {
+    float *pool;  // read by quantize, written by dequantize
+    int num_slots;
+    uint8_t *store;
+    float *scales;
+    int store_slots;
+    const int32_t *src, *dst;
+    int n, layers;
+    long long slot_values;
+    int block;
+    bool int8;  // else e4m3
+};
+cudaError_t launch_state_quantize(const StoreArgs &a, cudaStream_t stream);
+cudaError_t launch_state_dequantize(const StoreArgs &a, cudaStream_t stream);
+
+// Decode of up to K tokens a row.
+struct TokensArgs {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    float scale;
+    float *state;
+    const int32_t *slots, *counts;
+    void *out;  // NULL: no outputs
+    int N, K, num_slots, H, d;
+    kda_dtype dtype;
+    Prologue pro;
+    int write_state;
+};
+cudaError_t launch_decode_tokens(const TokensArgs &a, cudaStream_t stream);
+
 }  // namespace kda

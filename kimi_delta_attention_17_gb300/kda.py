@@ -264,6 +264,68 @@ def _launch_decode_slots(q, k, v, g, beta, scale, state, slots, out, opts, strea
     return out
 
 
+def decode_tokens(q, k, v, g, beta, scale, state, *, slots=None, counts=None, write_state=True,
+                  want_out=True, out=None, stream=None, decay="channel", gate="log", gate_lower=-5.0,
+                  l2norm_qk=False):
+    """Up to K tokens of each row in one pass over the states (kda_decode_tokens):
+    what K calls of decode_step compute, up to fp32 rounding. q, k [N, K, H, dk];
+    v [N, K, H, dv]; g [N, K, H, dk] fp32 (or by the decay); beta [N, K, H] fp32;
+    state [N, H, dk, dv] fp32, or a pool [P, H, dk, dv] with ``slots`` (int32 [N], as
+    in decode_step). ``counts`` (int32 [N], on the device): row n takes its first
+    counts[n] tokens; outputs behind them are zeros.
+    ``write_state=False`` leaves every state as it was (drafts to verify);
+    ``want_out=False`` forms no outputs (accepted tokens to commit).
+    Returns out [N, K, H, dv], or None. Options as in decode_step."""
+    _need(q, "q", ndim=4)
+    dtype = q.dtype
+    if dtype not in _DTYPES:
+        raise ValueError("q/k/v must be bfloat16 or float32")
+    _need(k, "k", dtype, 4)
+    _need(v, "v", dtype, 4)
+    _check_g(g, decay, 4)
+    _need(beta, "beta", torch.float32, 3)
+    _need(state, "state", torch.float32, 4)
+    shape = q.shape
+    N, K, H, dk = shape
+    rows, dv = (N, K, H), v.shape[3]
+    if k.shape != shape or v.shape[:3] != rows or beta.shape != rows:
+        raise ValueError("q, k, v and beta must share [N, K, H]")
+    if decay != "none" and g.shape != (shape if decay == "channel" else rows):
+        raise ValueError("g must be [N, K, H, dk], or [N, K, H] with the scalar decay")
+    if state.shape[1:] != (H, dk, dv):
+        raise ValueError("state must be [%s, H, dk, dv]" % ("N" if slots is None else "P"))
+    if slots is None and state.shape[0] != N:
+        raise ValueError("state must have one state per row")
+    for t, name in ((slots, "slots"), (counts, "counts")):
+        if t is not None:
+            _need(t, name, torch.int32, 1)
+            if t.shape[0] != N:
+                raise ValueError("%s must have one entry per row" % name)
+    if not (write_state or want_out):
+        raise ValueError("write_state and want_out leave nothing to do")
+    if out is not None:
+        _need(out, "out", dtype, 4)
+        if out.shape != v.shape or not want_out:
+            raise ValueError("out must have v's shape, and needs want_out")
+    return _on_stream(_launch_decode_tokens, ("q", "k", "v", "g", "beta", "state", "slots", "counts", "out"),
+                      (q, k, v, g if decay != "none" else None, beta, state, slots, counts, out), stream,
+                      q, k, v, g, beta, scale, state, slots, counts, out, write_state, want_out,
+                      _options(decay, gate, gate_lower, l2norm_qk))
+
+
+def _launch_decode_tokens(q, k, v, g, beta, scale, state, slots, counts, out, write_state, want_out, opts, stream):
+    if want_out and out is None:
+        out = torch.empty_like(v)
+    N, K, H, dk = q.shape
+    status = _lib.lib().kda_decode_tokens(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if g is None else g.data_ptr(), beta.data_ptr(), scale,
+        state.data_ptr(), _ptr(slots), _ptr(counts), _ptr(out), N, K, state.shape[0], H, dk, v.shape[3],
+        _DTYPES[q.dtype], None if opts is None else ctypes.byref(opts), bool(write_state), stream)
+    if status:
+        _lib.check("kda_decode_tokens", status)
+    return out
+
+
 def output_gate_rmsnorm(o, z, weight=None, eps=1e-6, *, out=None, stream=None):
     """out = weight * o / sqrt(mean(o^2 over d_v) + eps) * sigmoid(z), per token
     and head (kda_output_gate_rmsnorm). o, z [..., H, dv] of one dtype (bf16 or

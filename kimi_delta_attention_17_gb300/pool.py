@@ -1,4 +1,5 @@
-"""Binding of the state pool's maintenance (kda_state_copy, kda_state_compact).
+"""Binding of the state pool's maintenance (kda_state_copy, kda_state_compact) and
+of stores that hold states in 8 bits (kda_state_quantize, kda_state_dequantize).
 A pool is a tensor of slots, one per sequence: [P, ...] as decode_step and
 gated_scan_step take it with ``slots``, or [L, P, ...] over L layers."""
 import torch
@@ -97,3 +98,69 @@ def _launch_compact(pool, live, new_slot, count, slots, layers, nbytes, stream):
     if status:
         _lib.check("kda_state_compact", status)
     return new_slot, count
+
+
+_STORE_TYPES = {torch.int8: _lib.STORE["int8"], torch.float8_e4m3fn: _lib.STORE["e4m3"]}
+
+
+def _store_call(entry, pool, store, scales, src, dst, slot_dim, stream):
+    """Checks the arguments of state_quantize and state_dequantize and launches one."""
+    layers, slots, nbytes = _pool(pool, "pool", slot_dim)
+    if pool.dtype != torch.float32:
+        raise ValueError("pool must be float32")
+    _, store_slots, values = _pool(store, "store", slot_dim)
+    if store.dtype not in _STORE_TYPES:
+        raise ValueError("store must be int8 or float8_e4m3fn")
+    shape, kept = pool.shape, store.shape
+    if shape[:slot_dim] != kept[:slot_dim] or shape[slot_dim + 1:] != kept[slot_dim + 1:]:
+        raise ValueError("store must have the pool's layers and slot shape")
+    _need(scales, "scales", torch.float32)
+    if scales.dim() <= slot_dim or scales.shape[:slot_dim + 1] != kept[:slot_dim + 1]:
+        raise ValueError("scales must have the store's layers and slots")
+    per = scales.numel() // (layers * store_slots)
+    block = values // per if per and values % per == 0 else 0
+    if block not in (32, 64, 128):
+        raise ValueError("scales must hold one value for each 32, 64 or 128 of a slot's")
+    _need(src, "src", torch.int32, 1)
+    _need(dst, "dst", torch.int32, 1)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _on_stream(_launch_store, ("pool", "store", "scales", "src", "dst"), (pool, store, scales, src, dst), stream,
+               entry, pool, slots, store, scales, store_slots, src, dst, layers, values, block)
+
+
+def _launch_store(entry, pool, slots, store, scales, store_slots, src, dst, layers, values, block, stream):
+    lists = (src.data_ptr(), dst.data_ptr(), src.shape[0], layers, values, block, _STORE_TYPES[store.dtype], stream)
+    if entry == "kda_state_quantize":
+        status = _lib.lib().kda_state_quantize(pool.data_ptr(), slots, store.data_ptr(), scales.data_ptr(), store_slots,
+                                               *lists)
+    else:
+        status = _lib.lib().kda_state_dequantize(store.data_ptr(), scales.data_ptr(), store_slots, pool.data_ptr(),
+                                                 slots, *lists)
+    if status:
+        _lib.check(entry, status)
+
+
+def state_quantize(pool, src, store, scales, dst, *, slot_dim=0, stream=None):
+    """store[dst[i]] = pool[src[i]] in 8 bits, for every entry i (kda_state_quantize):
+    requests parked, or states of shared prefixes kept, at a quarter of their size.
+    ``pool`` fp32 and ``slot_dim`` as in state_copy. ``store`` int8 or float8_e4m3fn:
+    [S, ...], or [L, S, ...], with the pool's slot shape. ``scales`` fp32 [S, ...], or
+    [L, S, ...]: one for each 32, 64 or 128 consecutive values of a slot, e.g.
+    [S, H, dk] for states [S, H, dk, dv] (a scale for each key channel). With m the
+    largest magnitude of such a block, a value comes back within m / 254 (int8) or
+    2^-4 of itself (e4m3; within m / 458752 near zero).
+    ``src``, ``dst`` int32 [n] on the device, n <= 4096, as in state_copy: src -1
+    stores zeros, entries out of range are skipped, of entries that name one
+    destination the last holds. Returns (store, scales)."""
+    _store_call("kda_state_quantize", pool, store, scales, src, dst, slot_dim, stream)
+    return store, scales
+
+
+def state_dequantize(store, scales, src, pool, dst, *, slot_dim=0, stream=None):
+    """pool[dst[i]] = store[src[i]] as fp32 values, for every entry i
+    (kda_state_dequantize): the way back of state_quantize, with its arguments.
+    One source in several entries resumes several samples of a prefix. Returns
+    ``pool``."""
+    _store_call("kda_state_dequantize", pool, store, scales, src, dst, slot_dim, stream)
+    return pool
