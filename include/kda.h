@@ -783,7 +783,8 @@ typedef enum {
  *             out of range, or whose src is not below the source's slots, are
  *             skipped; of entries that name one destination the last holds
  *  n          0 .. KDA_STATE_COPY_MAX, else KDA_ERR_UNSUPPORTED
- *  block      32, 64 or 128; slot_values a positive multiple of it, at most 2^32
+ *  layers     1 .. 65535; block 32, 64 or 128; slot_values a positive multiple of
+ *             it, at most 2^32
  *  format     kda_store_format
  * Slots of pool and store 16-byte aligned, scales 4-byte. pool, store and scales
  * must not overlap. No workspace; one launch.

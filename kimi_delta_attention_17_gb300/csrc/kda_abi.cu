@@ -638,10 +638,6 @@ kda_status norm_check(const NormArgs &a) {
     return norm_types_ok(a.D, a.dtype, a.residual ? a.residual_dtype : KDA_DTYPE_F32);
 }
 
-size_t parts_bytes(long long rows_of_ctas, int most, int D) {
-    return (size_t)(rows_of_ctas < most ? rows_of_ctas : most) * (size_t)D * sizeof(float);
-}
-
 }  // namespace
 
 extern "C" kda_status kda_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps, void *out,
@@ -690,7 +686,7 @@ extern "C" kda_status kda_rmsnorm_quant(const void *x, const void *residual, con
 
 extern "C" size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D) {
     if (!norm_sizes_ok(rows, D) || norm_types_ok(D, KDA_DTYPE_F32, KDA_DTYPE_F32) != KDA_OK) return 0;
-    return parts_bytes(rows, kNormParts, D);
+    return (size_t)norm_bwd_parts(rows, D) * (size_t)D * sizeof(float);
 }
 
 extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd, const float *weight,
@@ -715,7 +711,8 @@ extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const flo
 
 extern "C" size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv) {
     if (tokens < 0 || H <= 0 || tokens >= (1LL << 34) / H || (dv != 64 && dv != 128)) return 0;
-    return parts_bytes(tokens * H, kGateParts, dv);
+    const long long rows = tokens * H;
+    return (size_t)(rows < kGateParts ? rows : kGateParts) * (size_t)dv * sizeof(float);
 }
 
 extern "C" kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z, const float *weight,
@@ -749,11 +746,7 @@ kda_status store_check(const StoreArgs &a, const void *reads, size_t reads_bytes
     const uintptr_t r = reinterpret_cast<uintptr_t>(reads), w = reinterpret_cast<uintptr_t>(writes);
     if (r < w + writes_bytes && w < r + reads_bytes) return KDA_ERR_INVALID_ARGUMENT;
     if (a.n > KDA_STATE_COPY_MAX) return KDA_ERR_UNSUPPORTED;
-    // The grid: a CTA for every 4096 values of every entry.
-    const long long pieces = (a.slot_values + 4095) / 4096;
-    return pieces * a.layers >= (1LL << 31) / KDA_STATE_COPY_MAX && pieces * a.layers * a.n >= (1LL << 31)
-               ? KDA_ERR_UNSUPPORTED
-               : KDA_OK;
+    return a.layers > 65535 ? KDA_ERR_UNSUPPORTED : KDA_OK;  // the grid's third dimension
 }
 
 bool store_sizes_ok(int num_slots, int store_slots, int layers, long long slot_values, int block) {

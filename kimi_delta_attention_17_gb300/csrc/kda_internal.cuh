@@ -197,8 +197,9 @@ struct NormArgs {
 };
 cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream);
 
-// Most CTAs of the norms' gradients, each of which leaves one row of a weight gradient's parts.
-constexpr int kNormParts = 608, kGateParts = 1216;
+// CTAs of the norms' gradients at most, each of which leaves one row of a weight gradient's parts.
+int norm_bwd_parts(long long rows, int D);
+constexpr int kGateParts = 1216;
 
 struct NormBwdArgs {
     const void *dy, *h;

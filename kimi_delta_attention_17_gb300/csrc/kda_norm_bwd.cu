@@ -13,126 +13,198 @@
 namespace kda {
 namespace {
 
-constexpr int kBwdCta = 256;  // threads of a CTA whose rows take a warp or less
+// The launch that follows with cudaLaunchAttributeProgrammaticStreamSerialization may start once every CTA
+// has said this (or ended); it waits for this kernel's writes by itself.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 
+constexpr int kSms = 152;
+
+RowThreads bwd_threads(int D) { return D <= 512 ? RowThreads{256, D <= 256 ? 1 : 2} : row_threads(D); }
+
+// CTAs that an SM runs at once, by the registers that the kernels below take: what is launched, so that no rows
+// wait for a second round.
+int ctas_per_sm(int D) {
+    const RowThreads s = bwd_threads(D);
+    if (D <= 512) return 2;
+    return s.groups == 1 ? 1024 / s.threads : s.groups == 2 && s.threads <= 256 ? 512 / s.threads : 1;
+}
+
+// Threads of a row: kTpr lanes of a CTA of 256 threads (8, 16 or 32), or the whole CTA (0).
 template <int kTpr>
 struct BwdShape {
-    static constexpr int threads = kTpr > 32 ? kTpr : kBwdCta;
-    static constexpr int rows = threads / kTpr;
-    static constexpr int lanes = kTpr > 32 ? 32 : kTpr;
-    static constexpr int warps = kTpr > 32 ? kTpr / 32 : 1;
+    static constexpr int lanes = kTpr ? kTpr : 32;
+    static constexpr int threads = 256;  // of a CTA, kTpr > 0
+    static constexpr int rows = kTpr ? threads / kTpr : 1;  // at a time
 };
 
-template <typename X, typename Hh, int kTpr, int kGroups>
-__global__ void __launch_bounds__(BwdShape<kTpr>::threads)
+// A CTA takes rows in turn: kPasses of them for each of its teams of threads. With 16-bit rows the next ones'
+// loads are on their way while it works on one (32768 x 2048, bf16: 104 us without, 92 with; with an fp32 h
+// enough is in flight: 166 us, and 179 with it).
+template <typename X, typename Hh, int kTpr, int kGroups, int kPasses, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas)
 rmsnorm_bwd_kernel(const X *dy, const Hh *__restrict__ h, const float *__restrict__ rstd,
                    const float *__restrict__ w, const Hh *dh, X *dx, Hh *dres,  // may be in place
                    float *__restrict__ part, long long rows, int D) {
     using S = BwdShape<kTpr>;
-    extern __shared__ float smem[];  // the rows' weight gradients, where a CTA has several rows
-    __shared__ float sums[2][32];
-    const int lane = threadIdx.x % kTpr, warp = threadIdx.x >> 5, sub = threadIdx.x / kTpr;
+    extern __shared__ float rows_dw[];  // [S::rows][D], where a CTA has several rows
+    __shared__ __align__(16) float sums[2][32];
+    const int threads = kTpr ? S::threads : blockDim.x;
+    const int tpr = kTpr ? kTpr : threads, lane = kTpr ? threadIdx.x % kTpr : threadIdx.x, sub = kTpr ? threadIdx.x / tpr : 0;
+    const int warp = threadIdx.x >> 5, warps = threads >> 5;
     const int groups = D / 8;
-    float wv[kGroups][8], dw[kGroups][8];
+    // Up to 16 values a thread the weights, u and n stay in registers. Wider rows form them again after the sum:
+    // from the row as it was loaded (16 bits), or from the L2 cache.
+    constexpr bool kKeep = kGroups <= 2, kRaw = !kKeep && sizeof(Hh) == 2 && kThreads <= 512;
+    constexpr bool kNext = kKeep && sizeof(Hh) == 2;
+    float wv[kKeep ? kGroups : 1][8], dw[kGroups][8];
+    auto weights = [&](int i, float *v) {
+        const int c = lane + i * tpr;
+        if (w && c < groups) {
+            unpack8(load8(w + 8 * c), v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 1.f;
+        }
+    };
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const int c = lane + i * kTpr;
+        if constexpr (kKeep) weights(i, wv[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            wv[i][j] = c < groups ? (w ? w[8 * c + j] : 1.f) : 0.f;
-            dw[i][j] = 0.f;
-        }
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
     }
+    if (!kTpr && warp == 0) sums[0][threadIdx.x] = sums[1][threadIdx.x] = 0.f;
+    if (!kTpr) __syncthreads();
+    Raw8<X> ry[kPasses][kGroups];
+    Raw8<Hh> rh[kPasses][kGroups], rd[kPasses][kGroups];
+    float r_next[kPasses];
+    auto load = [&](long long row0) {
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const long long row = row0 + p * S::rows;
+            if (row >= rows) break;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int c = lane + i * tpr;
+                if (c >= groups) break;
+                const size_t at = (size_t)row * D + 8 * c;
+                ry[p][i] = load8(dy + at);
+                rh[p][i] = load8(h + at);
+                if (dh) rd[p][i] = load8(dh + at);
+            }
+            r_next[p] = rstd[row];
+        }
+    };
+    const long long step = (long long)gridDim.x * (S::rows * kPasses);
+    const long long start = (long long)blockIdx.x * (S::rows * kPasses);
+    if (kNext) load(start + sub);
     int flip = 0;
     const float inv_d = 1.f / (float)D;
-    for (long long first = (long long)blockIdx.x * S::rows; first < rows; first += (long long)gridDim.x * S::rows) {
-        const long long row = first + sub;
-        const bool live = row < rows;
-        const size_t base = (size_t)(live ? row : 0) * D;
-        Raw8<X> ry[kGroups];
-        Raw8<Hh> rh[kGroups], rd[kGroups];
+    for (long long first = start; first < rows; first += step) {
+        if (!kNext) load(first + sub);
+        float r[kPasses], un[kPasses], u[kPasses][kKeep ? kGroups : 1][8], n[kPasses][kKeep ? kGroups : 1][8];
+        Raw8<Hh> cd[kPasses][kGroups];
+        auto inside = [&](int p, int i) { return first + sub + p * S::rows < rows && lane + i * tpr < groups; };
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const int c = lane + i * kTpr;
-            if (live && c < groups) {
-                ry[i] = load8(dy + base + 8 * c);
-                rh[i] = load8(h + base + 8 * c);
-                if (dh) rd[i] = load8(dh + base + 8 * c);
+        for (int p = 0; p < kPasses; ++p) {
+            r[p] = r_next[p];
+            un[p] = 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int k = kKeep ? i : 0;
+                unpack8(ry[p][i], u[p][k]);
+                unpack8(rh[p][i], n[p][k]);
+                cd[p][i] = rd[p][i];
+                if constexpr (!kKeep) weights(i, wv[0]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (!inside(p, i)) u[p][k][j] = n[p][k][j] = 0.f;
+                    else n[p][k][j] *= r[p];
+                    dw[i][j] += u[p][k][j] * n[p][k][j];
+                    u[p][k][j] *= wv[k][j];
+                    un[p] += u[p][k][j] * n[p][k][j];
+                }
             }
         }
-        const float r = live ? rstd[row] : 0.f;
-        float un = 0.f;
-        float u[kGroups][8], n[kGroups][8];
+        if (kNext) load(first + sub + step);
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const bool in = live && lane + i * kTpr < groups;
-            unpack8(ry[i], u[i]);
-            unpack8(rh[i], n[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (!in) u[i][j] = n[i][j] = 0.f;
-                n[i][j] *= r;
-                dw[i][j] += u[i][j] * n[i][j];
-                u[i][j] *= wv[i][j];
-                un += u[i][j] * n[i][j];
+        for (int p = 0; p < kPasses; ++p) {
+            un[p] = lanes_sum<S::lanes>(un[p]);
+            if constexpr (kTpr == 0) {
+                if ((threadIdx.x & 31) == 0) sums[flip][warp] = un[p];
+                __syncthreads();  // the other half of `sums` is read no more: one barrier a row
+                un[p] = 0.f;
+                for (int i = 0; i < warps; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sums[flip][i]);
+                    un[p] += (v.x + v.y) + (v.z + v.w);
+                }
+                flip ^= 1;
             }
-        }
-        un = lanes_sum<S::lanes>(un);
-        if constexpr (S::warps > 1) {
-            if ((threadIdx.x & 31) == 0) sums[flip][warp] = un;
-            __syncthreads();  // the other half of `sums` is read no more: one barrier a row
-            un = 0.f;
+            un[p] *= inv_d;
 #pragma unroll
-            for (int i = 0; i < S::warps; ++i) un += sums[flip][i];
-            flip ^= 1;
-        }
-        un *= inv_d;
+            for (int i = 0; i < kGroups; ++i) {
+                if (!inside(p, i)) continue;
+                const size_t at = (size_t)(first + sub + p * S::rows) * D + 8 * (lane + i * tpr);
+                const int k = kKeep ? i : 0;
+                if constexpr (!kKeep) {
+                    if constexpr (kRaw) {
+                        unpack8(ry[p][i], u[p][0]);
+                        unpack8(rh[p][i], n[p][0]);
+                    } else {
+                        unpack8(load8(dy + at), u[p][0]);
+                        unpack8(load8(h + at), n[p][0]);
+                        if (dh) cd[p][i] = load8(dh + at);
+                    }
+                    weights(i, wv[0]);
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const int c = lane + i * kTpr;
-            if (!(live && c < groups)) continue;
-            float d[8];
-            if (dh) {
-                unpack8(rd[i], d);
-            } else {
+                    for (int j = 0; j < 8; ++j) {
+                        n[p][0][j] *= r[p];
+                        u[p][0][j] *= wv[0][j];
+                    }
+                }
+                float d[8];
+                if (dh) {
+                    unpack8(cd[p][i], d);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = 0.f;
+                    for (int j = 0; j < 8; ++j) d[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] += r[p] * (u[p][k][j] - n[p][k][j] * un[p]);
+                store8(dx + at, d);
+                if (dres) store8(dres + at, d);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] += r * (u[i][j] - n[i][j] * un);
-            store8(dx + base + 8 * c, d);
-            if (dres) store8(dres + base + 8 * c, d);
         }
     }
+    dependents_may_start();
     if (!part) return;
     if constexpr (S::rows > 1) {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int c = lane + i * kTpr;
-            if (c < groups) store8(smem + (size_t)sub * D + 8 * c, dw[i]);
+            const int c = lane + i * tpr;
+            if (c < groups) store8(rows_dw + (size_t)sub * D + 8 * c, dw[i]);
         }
         __syncthreads();
         for (int c = threadIdx.x; c < D; c += S::threads) {
             float t = 0.f;
-            for (int s = 0; s < S::rows; ++s) t += smem[(size_t)s * D + c];
+            for (int s = 0; s < S::rows; ++s) t += rows_dw[(size_t)s * D + c];
             part[(size_t)blockIdx.x * D + c] = t;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const int c = lane + i * kTpr;
+            const int c = lane + i * tpr;
             if (c < groups) store8(part + (size_t)blockIdx.x * D + 8 * c, dw[i]);
         }
     }
 }
 
-template <typename X, typename Hh, int kTpr, int kGroups>
-cudaError_t launch_bwd_k(const NormBwdArgs &a, cudaStream_t stream) {
+template <typename X, typename Hh, int kTpr, int kGroups, int kPasses, int kThreads, int kCtas>
+cudaError_t launch_bwd_k(const NormBwdArgs &a, int threads, cudaStream_t stream) {
     using S = BwdShape<kTpr>;
-    const long long want = (a.rows + S::rows - 1) / S::rows;
-    const unsigned blocks = (unsigned)(want < kNormParts ? want : kNormParts);
+    const long long per = S::rows * kPasses, want = (a.rows + per - 1) / per, most = kSms * ctas_per_sm(a.D);
+    const unsigned blocks = (unsigned)(want < most ? want : most);
     const size_t smem = a.dweight && S::rows > 1 ? (size_t)S::rows * a.D * sizeof(float) : 0;
-    rmsnorm_bwd_kernel<X, Hh, kTpr, kGroups><<<blocks, S::threads, smem, stream>>>(
+    rmsnorm_bwd_kernel<X, Hh, kTpr, kGroups, kPasses, kThreads, kCtas><<<blocks, threads, smem, stream>>>(
         static_cast<const X *>(a.dy), static_cast<const Hh *>(a.h), a.rstd, a.w, static_cast<const Hh *>(a.dh),
         static_cast<X *>(a.dx), static_cast<Hh *>(a.dres), a.dweight ? a.part : nullptr, a.rows, a.D);
     const cudaError_t err = cudaGetLastError();
@@ -141,16 +213,16 @@ cudaError_t launch_bwd_k(const NormBwdArgs &a, cudaStream_t stream) {
 
 template <typename X, typename Hh>
 cudaError_t launch_bwd_t(const NormBwdArgs &a, cudaStream_t stream) {
-    if (a.D <= 64) return launch_bwd_k<X, Hh, 8, 1>(a, stream);
-    if (a.D <= 128) return launch_bwd_k<X, Hh, 16, 1>(a, stream);
-    if (a.D <= 256) return launch_bwd_k<X, Hh, 32, 1>(a, stream);
-    if (a.D <= 512) return launch_bwd_k<X, Hh, 64, 1>(a, stream);
-    if (a.D <= 1024) return launch_bwd_k<X, Hh, 128, 1>(a, stream);
-    if (a.D <= 2048) return launch_bwd_k<X, Hh, 256, 1>(a, stream);
-    if (a.D <= 4096) return launch_bwd_k<X, Hh, 512, 1>(a, stream);
-    if (a.D <= 8192) return launch_bwd_k<X, Hh, 1024, 1>(a, stream);
-    if (a.D <= 16384) return launch_bwd_k<X, Hh, 1024, 2>(a, stream);
-    return launch_bwd_k<X, Hh, 1024, 4>(a, stream);
+    const RowThreads s = bwd_threads(a.D);
+    if (a.D <= 64) return launch_bwd_k<X, Hh, 8, 1, 2, 256, 2>(a, s.threads, stream);
+    if (a.D <= 128) return launch_bwd_k<X, Hh, 16, 1, 2, 256, 2>(a, s.threads, stream);
+    if (a.D <= 256) return launch_bwd_k<X, Hh, 32, 1, 2, 256, 2>(a, s.threads, stream);
+    if (a.D <= 512) return launch_bwd_k<X, Hh, 32, 2, 1, 256, 2>(a, s.threads, stream);
+    if (s.groups == 1) return launch_bwd_k<X, Hh, 0, 1, 1, 512, 2>(a, s.threads, stream);
+    if (s.groups == 2 && s.threads <= 256) return launch_bwd_k<X, Hh, 0, 2, 1, 256, 2>(a, s.threads, stream);
+    if (s.groups == 2) return launch_bwd_k<X, Hh, 0, 2, 1, 512, 1>(a, s.threads, stream);
+    if (s.threads <= 512) return launch_bwd_k<X, Hh, 0, 4, 1, 512, 1>(a, s.threads, stream);
+    return launch_bwd_k<X, Hh, 0, 4, 1, 1024, 1>(a, s.threads, stream);
 }
 
 // ---- the output gate
@@ -206,6 +278,7 @@ gate_bwd_kernel(const T *dout, const T *o, const T *z, const float *__restrict__
         *reinterpret_cast<uint4 *>(d_o + at) = pack16<T>(x);
         *reinterpret_cast<uint4 *>(dz + at) = pack16<T>(c);
     }
+    dependents_may_start();
     if (!part) return;
 #pragma unroll
     for (int j = 0; j < E; ++j) sums[sub][E * li + j] = dw[j];
@@ -235,6 +308,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
     __shared__ float sums[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float t = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
     if (c < D)
         for (int p = threadIdx.y; p < parts; p += 32) t += part[(size_t)p * D + c];
     sums[threadIdx.y][threadIdx.x] = t;
@@ -247,8 +321,22 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict
 }  // namespace
 
 cudaError_t launch_sum_parts(const float *part, int parts, int D, float *dweight, cudaStream_t stream) {
-    sum_parts_kernel<<<(D + 31) / 32, dim3(32, 32), 0, stream>>>(part, parts, D, dweight);
-    return cudaGetLastError();
+    // Launched as the kernel before it ends: what it needs of a launch's time is over when the parts are there.
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((D + 31) / 32);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_parts_kernel, part, parts, D, dweight);
+}
+
+int norm_bwd_parts(long long rows, int D) {
+    const int most = kSms * ctas_per_sm(D);
+    return rows < most ? (int)rows : most;
 }
 
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs &a, cudaStream_t stream) {

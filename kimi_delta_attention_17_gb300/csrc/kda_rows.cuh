@@ -72,6 +72,18 @@ __device__ __forceinline__ void store8(float *p, const float *x) {
     *reinterpret_cast<uint4 *>(p + 4) = pack16<float>(x + 4);
 }
 
+// How a CTA holds a row of D > 512 values: groups of 8 a thread, and whole warps.
+struct RowThreads {
+    int threads, groups;
+};
+inline RowThreads row_threads(int D) {
+    const auto warps = [D](int groups) { return ((D / 8 + groups - 1) / groups + 31) / 32; };
+    // Two groups a thread, or one where that leaves fewer lanes idle; four where two would take more than 512
+    // threads.
+    const int groups = D > 8192 ? 4 : D <= 4096 && warps(1) < 2 * warps(2) ? 1 : 2;
+    return {32 * warps(groups), groups};
+}
+
 // Sum over `kLanes` neighbouring lanes (a power of two), in all of them.
 template <int kLanes>
 __device__ __forceinline__ float lanes_sum(float x) {

@@ -116,7 +116,7 @@ def test_store_refusals(L, name):
                 dict(pool=FAKE + 8), dict(store=far + 8), dict(scales=far + 2), dict(src=FAKE + 2), dict(dst=FAKE + 1),
                 dict(store=FAKE + 16), dict(store=FAKE + 4 * 256 * 2 * 4 - 16)):
         assert call(**bad) == INVALID, bad
-    assert call(n=4096, values=2 ** 32, layers=1) == UNSUPPORTED  # more CTAs than a grid holds
+    assert call(n=4096, layers=65536) == UNSUPPORTED
     assert call(n=0) == OK
 
 
