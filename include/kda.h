@@ -627,6 +627,9 @@ kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live, int
                              int32_t *count, int layers, size_t slot_bytes, void *workspace,
                              size_t workspace_bytes, cudaStream_t stream);
 
+/* Most tokens a row of one kda_decode_tokens call. */
+#define KDA_DECODE_TOKENS_MAX (1 << 23)
+
 /*
  * One call for up to K tokens of each of N rows: what K calls of
  * kda_decode_step_slots compute, in one pass over the states (drafts to verify,
@@ -645,8 +648,11 @@ kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live, int
  *  out        written, or NULL where no outputs are wanted
  *  write_state nonzero: the states after the rows' last tokens are written;
  *             0: no state is changed. Without outputs it must be nonzero
- * Results equal the single steps' up to fp32 rounding. No workspace; options
- * and errors as kda_decode_step_opt.
+ *  K          0 .. KDA_DECODE_TOKENS_MAX
+ * Results equal the single steps' up to fp32 rounding: products are formed from
+ * operands split in two, to some 2^-22 of their magnitudes; a state that keeps
+ * its values (decays of 1, nothing written) keeps them exactly. No workspace;
+ * options and errors as kda_decode_step_opt.
  */
 kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const float *g,
                              const float *beta, float scale, float *state, const int32_t *slots,

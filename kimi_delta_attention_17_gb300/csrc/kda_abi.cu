@@ -792,7 +792,7 @@ extern "C" kda_status kda_decode_tokens(const void *q, const void *k, const void
     if (N < 0 || K < 0 || H <= 0 || dk <= 0 || dv <= 0 || num_slots < 0 || !isfinite(scale)) return KDA_ERR_INVALID_ARGUMENT;
     if (N > 0 && (slots ? num_slots == 0 : num_slots != N)) return KDA_ERR_INVALID_ARGUMENT;
     if ((long long)N * H >= (1LL << 31) || (long long)num_slots * H >= (1LL << 31)) return KDA_ERR_INVALID_ARGUMENT;
-    if ((long long)N * H >= (1LL << 46) / (K > 0 ? K : 1) / dk) return KDA_ERR_INVALID_ARGUMENT;
+    if (K > KDA_DECODE_TOKENS_MAX || (long long)N * H >= (1LL << 46) / (K > 0 ? K : 1) / dk) return KDA_ERR_INVALID_ARGUMENT;
     const bool some = N > 0 && K > 0;
     if (some && (!q || !k || !v || !beta || !state || (!out && !write_state))) return KDA_ERR_INVALID_ARGUMENT;
     if (!g_ok(g, a.pro, some)) return KDA_ERR_INVALID_ARGUMENT;
