@@ -696,7 +696,7 @@ kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const vo
  *  residual_out [rows][D], residual_dtype (written): h, rounded to that type;
  *             what is normalised is h as it stands there, so that the backward
  *             call, which reads it, takes the same values. Given where residual
- *             is, and may alias it exactly
+ *             is, and may alias it (or an x of its type) exactly
  *  rstd       [rows] fp32 (written), or NULL: 1 / sqrt(mean h^2 + eps), for
  *             kda_rmsnorm_bwd
  *  dtype, residual_dtype: (BF16, BF16), (BF16, F32) or (F32, F32); (F32, BF16)

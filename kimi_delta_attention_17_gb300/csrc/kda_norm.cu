@@ -28,7 +28,7 @@ struct RowShape {
 
 template <typename X, typename R, bool kQuant, int kTpr, int kGroups, int kPasses, int kThreads>
 __global__ void __launch_bounds__(kThreads)
-rmsnorm_kernel(const X *__restrict__ x, const R *residual, const float *__restrict__ w, float eps,
+rmsnorm_kernel(const X *x, const R *residual, const float *__restrict__ w, float eps,
                X *__restrict__ out, uint8_t *__restrict__ q, float *__restrict__ scales, int scale_block,
                R *residual_out, float *__restrict__ rstd, long long rows, int D) {
     using S = RowShape<kTpr>;
@@ -193,8 +193,7 @@ cudaError_t launch_fwd_q(const NormArgs &a, cudaStream_t stream) {
     if (a.D <= 128) return launch_fwd_k<X, R, kQuant, 16, 1, 2, T>(a, T, stream);
     if (a.D <= 256) return launch_fwd_k<X, R, kQuant, 32, 1, 2, T>(a, T, stream);
     if (a.D <= 512) return launch_fwd_k<X, R, kQuant, 32, 2, 1, T>(a, T, stream);
-    const RowThreads s = row_threads(a.D);
-    if (s.groups == 1) return launch_fwd_k<X, R, kQuant, 0, 1, 1, 512>(a, s.threads, stream);
+    const RowThreads s = row_threads(a.D, false);
     if (s.groups == 2) return launch_fwd_k<X, R, kQuant, 0, 2, 1, 512>(a, s.threads, stream);
     if (s.threads <= 512) return launch_fwd_k<X, R, kQuant, 0, 4, 1, 512>(a, s.threads, stream);
     return launch_fwd_k<X, R, kQuant, 0, 4, 1, 1024>(a, s.threads, stream);

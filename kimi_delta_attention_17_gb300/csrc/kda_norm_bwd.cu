@@ -19,7 +19,7 @@ __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepco
 
 constexpr int kSms = 152;
 
-RowThreads bwd_threads(int D) { return D <= 512 ? RowThreads{256, D <= 256 ? 1 : 2} : row_threads(D); }
+RowThreads bwd_threads(int D) { return D <= 512 ? RowThreads{256, D <= 256 ? 1 : 2} : row_threads(D, true); }
 
 // CTAs that an SM runs at once, by the registers that the kernels below take: what is launched, so that no rows
 // wait for a second round.
