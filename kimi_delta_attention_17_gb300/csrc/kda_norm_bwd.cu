@@ -303,19 +303,24 @@ cudaError_t launch_gate_bwd(const GateBwdArgs &a, cudaStream_t stream) {
     return err != cudaSuccess || !a.dweight ? err : launch_sum_parts(a.part, (int)blocks, D, a.dweight, stream);
 }
 
-// One CTA for 32 columns: 32 rows of threads take every 32nd part.
-__global__ void __launch_bounds__(1024) sum_parts_kernel(const float *__restrict__ part, int parts, int D, float *dweight) {
-    __shared__ float sums[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+// One CTA for 8 columns, its rows of threads sharing out the parts: 128 rows for many parts, 32 for few (1216 parts
+// of 128 columns took 8.6 us with 32 columns and 32 rows of threads a CTA: four CTAs, 38 loads in turn).
+constexpr int kSumCols = 8;
+__global__ void __launch_bounds__(kSumCols * 128)
+sum_parts_kernel(const float *__restrict__ part, int parts, int D, float *__restrict__ dweight) {
+    __shared__ float sums[kSumCols][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, x = lane % kSumCols;
+    const int c = blockIdx.x * kSumCols + x;  // D is a multiple of 8
     float t = 0.f;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-    if (c < D)
-        for (int p = threadIdx.y; p < parts; p += 32) t += part[(size_t)p * D + c];
-    sums[threadIdx.y][threadIdx.x] = t;
+    for (int p = threadIdx.x / kSumCols; p < parts; p += blockDim.x / kSumCols) t += part[(size_t)p * D + c];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if (lane < kSumCols) sums[x][warp] = t;
     __syncthreads();
-    t = lanes_sum<32>(sums[threadIdx.x][threadIdx.y]);
-    const int to = blockIdx.x * 32 + threadIdx.y;
-    if (threadIdx.x == 0 && to < D) dweight[to] = t;
+    if (warp >= kSumCols) return;
+    t = lanes_sum<32>(lane < blockDim.x / 32 ? sums[warp][lane] : 0.f);
+    if (lane == 0) dweight[blockIdx.x * kSumCols + warp] = t;
 }
 
 }  // namespace
@@ -326,8 +331,8 @@ cudaError_t launch_sum_parts(const float *part, int parts, int D, float *dweight
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((D + 31) / 32);
-    cfg.blockDim = dim3(32, 32);
+    cfg.gridDim = dim3(D / kSumCols);
+    cfg.blockDim = dim3(kSumCols * (parts > 256 ? 128 : 32));
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
