@@ -1,5 +1,6 @@
 """Kimi Delta Attention gated delta-rule scan for GB300 (sm_103a), the gated linear
-recurrence beside it, and the pool of states that a serving loop keeps.
+recurrence beside it, the norms around both, and the pool of states that a serving
+loop keeps, in fp32 or parked in 8 bits.
 
 The compute lives in libkda.so (C ABI: include/kda.h); this package is its thin
 Python binding plus the seeded synthetic-input generator. Importing the package

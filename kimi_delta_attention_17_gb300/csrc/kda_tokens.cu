@@ -444,10 +444,11 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
 #pragma unroll
             for (int i = 0; i < KT; ++i)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    some_of<4>(S[r] + 8 * i * kCols, s[i][r]);
-                    if (!here) s[i][r][0] = s[i][r][1] = s[i][r][2] = s[i][r][3] = __uint_as_float(0x7fffffffu);
-                }
+                for (int r = 0; r < 2; ++r) some_of<4>(S[r] + 8 * i * kCols, s[i][r]);
+            if (!here) {
+#pragma unroll
+                for (int i = 0; i < KT * 8; ++i) s[i / 8][i / 4 % 2][i % 4] = __uint_as_float(0x7fffffffu);
+            }
         }
 
         float(*tr)[TokenSmem<D, InT>::kTrans] = sm.trans[warp], (*other)[TokenSmem<D, InT>::kTrans] = sm.trans[warp ^ 1];
@@ -458,10 +459,11 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
             constexpr int kN = decltype(n)::value;
             constexpr bool kBoth = kN <= kBlock / 2;
             // The warp's part of P and R, 32 columns by kN tokens each: in one product where the eight vectors of its n
-            // are k's and q's, else in two.
-            float acc[kBoth ? 1 : 2][2][4];
+            // are k's and q's, else in two. The small products have sums of their own: an MMA's sum is cut off, not
+            // rounded, so the fewer at full size the better.
+            float acc[kBoth ? 1 : 2][2][4], small[kBoth ? 1 : 2][2][4];
 #pragma unroll
-            for (int i = 0; i < (kBoth ? 8 : 16); ++i) acc[i >> 3][i >> 2 & 1][i & 3] = 0.f;
+            for (int i = 0; i < (kBoth ? 8 : 16); ++i) acc[i >> 3][i >> 2 & 1][i & 3] = small[i >> 3][i >> 2 & 1][i & 3] = 0.f;
             const float *from = (kBoth ? bl.read[y >> 2][y & 3] : bl.read[0][y]) + 2 * top + 4 * x;
             const float *from_q = bl.read[1][y] + 2 * top + 4 * x;
 #pragma unroll
@@ -485,7 +487,8 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const float4 v4 = b ? b1 : b0;
-                            mma_tf32(acc[b][m], part == 1 ? lo[m] : hi[m], part == 2 ? v4.z : v4.x, part == 2 ? v4.w : v4.y);
+                            mma_tf32(part ? small[b][m] : acc[b][m], part == 1 ? lo[m] : hi[m], part == 2 ? v4.z : v4.x,
+                                     part == 2 ? v4.w : v4.y);
                         }
             }
             // A lane takes one column over all tokens, the sum of both warps' parts: both solve for e, each forms the
@@ -493,7 +496,9 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
 #pragma unroll
             for (int b = 0; b < (kBoth ? 1 : 2); ++b) {
                 const int to = kBoth ? 2 * x + (x & 2) * (kBlock / 4) : b * kBlock + 2 * x;  // R's rows begin at kBlock
-                const auto &d = acc[b];
+                auto &d = acc[b];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i >> 2][i & 3] += small[b][i >> 2][i & 3];
                 *reinterpret_cast<float4 *>(&tr[to][4 * y]) = make_float4(d[0][0], d[0][2], d[1][0], d[1][2]);
                 *reinterpret_cast<float4 *>(&tr[to + 1][4 * y]) = make_float4(d[0][1], d[0][3], d[1][1], d[1][3]);
             }
@@ -546,7 +551,8 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
 #pragma unroll
             for (int t = 0; t < kBlock; ++t) tr[t][lane] = ke[t];
             __syncwarp();
-            // S <- G_C S + k e^T, the same registers as accumulators.
+            // S <- G_C S + k e^T: the products' sums by themselves, and one rounded fp32 step to the state (added to it
+            // by the MMAs, whose sums are cut off, a slowly decaying state would lose 1e-7 of itself every block).
             float hi[2][4], lo[2][4];
             {
                 float e[2][4];
@@ -567,11 +573,7 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
                 const float2 tot = *reinterpret_cast<const float2 *>(&bl.total[at + 2 * x]);
                 const float2 w0 = *reinterpret_cast<const float2 *>(&bl.write[x][2 * (at + y)]);
                 const float2 w1 = *reinterpret_cast<const float2 *>(&bl.write[x + 4][2 * (at + y)]);
-                float c[2][4];
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) c[m][j] = (j & 1 ? tot.y : tot.x) * s[i][j & 1][2 * m + (j >> 1)];
+                float c[2][4] = {};
 #pragma unroll
                 for (int m = 0; m < 2; ++m) mma_tf32(c[m], lo[m], w0.x, w1.x);
 #pragma unroll
@@ -581,7 +583,10 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][j & 1][2 * m + (j >> 1)] = c[m][j];
+                    for (int j = 0; j < 4; ++j) {
+                        float &w = s[i][j & 1][2 * m + (j >> 1)];
+                        w = fmaf(j & 1 ? tot.y : tot.x, w, c[m][j]);
+                    }
             }
             if (last) {
 #pragma unroll

@@ -209,6 +209,27 @@ def test_streams_and_graphs():
         assert torch.equal(got, want) and torch.equal(held, state)
 
 
+@pytest.mark.parametrize("K", [3, 8])
+def test_thousands_of_tokens_do_not_drift(K):
+    """400 calls without decay, little written by each: a state that is rounded once a call is off by at most half a
+    unit of its last place each time (400 x 2^-24 of its magnitudes), and what is written, 1e-3 of it, by far less."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    S = n(2, 2, 128, 128) * 0.1
+    exact = S.double()
+    beta = torch.full((2, K, 2), 1e-3, device="cuda")
+    for _ in range(400):
+        q, v, k = n(2, K, 2, 128), n(2, K, 2, 128), torch.nn.functional.normalize(n(2, K, 2, 128), dim=-1)
+        decode_tokens(q, k, v, None, beta, 0.1, S, decay="none", want_out=False)
+        for t in range(K):
+            kt = k[:, t].double()
+            e = 1e-3 * (v[:, t].double() - torch.einsum("nhij,nhi->nhj", exact, kt))
+            exact += kt[..., None] * e[:, :, None]
+    beta64 = float(torch.tensor(1e-3, dtype=F))  # the oracle's 1e-3 is off by 2^-25 of itself: nothing beside the bound
+    assert abs(beta64 - 1e-3) < 1e-10
+    assert ((S.double() - exact).norm() / exact.norm()).item() <= 430 * 2.0 ** -24
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """A pool of 2^31 + values: 2100 slots of 64 heads of 128 x 128 have 2.2e9."""
