@@ -705,7 +705,8 @@ kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const vo
  *  rows       0 .. 2^31 - 1;  D a multiple of 8, at most 32768, else
  *             KDA_ERR_UNSUPPORTED
  * Pointers 16-byte aligned (rstd 4-byte). Outputs must not overlap inputs or one
- * another, but for residual_out. Sums are fp32. No workspace; one launch.
+ * another, but for residual_out; an out that is x, residual or residual_out is
+ * refused. Sums are fp32. No workspace; one launch.
  */
 kda_status kda_rmsnorm_fwd(const void *x, const void *residual, const float *weight, float eps,
                            void *out, void *residual_out, float *rstd, long long rows, int D,
@@ -752,8 +753,8 @@ size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D);
  *  dweight    [D] fp32 (written), or NULL where it is not wanted
  *  workspace  kda_rmsnorm_bwd_workspace_size(rows, D) bytes, 256-byte aligned,
  *             where dweight is given; contents on entry are ignored
- * dx may alias dout, and dresidual dh, exactly. Sums are fp32 in a fixed order (no
- * atomics). Types, sizes and alignment as the forward call.
+ * dx may alias dout, or a dh of its type, and dresidual dh, exactly. Sums are fp32
+ * in a fixed order (no atomics). Types, sizes and alignment as the forward call.
  */
 kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd,
                            const float *weight, const void *dh, void *dx, void *dresidual,

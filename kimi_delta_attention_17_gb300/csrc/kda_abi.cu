@@ -635,6 +635,9 @@ kda_status norm_check(const NormArgs &a) {
     for (const void *p : tensors)
         if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned4(a.rstd) || !aligned4(a.scales)) return KDA_ERR_INVALID_ARGUMENT;
+    // Where out is what h is, or comes from, the caller would have no h.
+    for (const void *p : {a.x, a.residual, (const void *)a.residual_out})
+        if (p && (p == a.out || p == a.q)) return KDA_ERR_INVALID_ARGUMENT;
     return norm_types_ok(a.D, a.dtype, a.residual ? a.residual_dtype : KDA_DTYPE_F32);
 }
 
@@ -699,6 +702,7 @@ extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const flo
     for (const void *p : tensors)
         if (!aligned16(p)) return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned4(rstd) || !aligned4(dweight)) return KDA_ERR_INVALID_ARGUMENT;
+    if (dx && dx == dresidual) return KDA_ERR_INVALID_ARGUMENT;
     const kda_status st = norm_types_ok(D, dtype, h_dtype);
     if (st != KDA_OK) return st;
     if (dweight && rows > 0 && (!workspace || workspace_bytes < kda_rmsnorm_bwd_workspace_size(rows, D)))
@@ -726,6 +730,7 @@ extern "C" kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *
     if (!aligned16(dout) || !aligned16(o) || !aligned16(z) || !aligned16(d_o) || !aligned16(dz))
         return KDA_ERR_INVALID_ARGUMENT;
     if (!aligned4(weight) || !aligned4(dweight)) return KDA_ERR_INVALID_ARGUMENT;
+    if (d_o && d_o == dz) return KDA_ERR_INVALID_ARGUMENT;
     if (dv != 64 && dv != 128) return KDA_ERR_UNSUPPORTED;
     if (dweight && tokens > 0 &&
         (!workspace || workspace_bytes < kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv)))

@@ -120,8 +120,8 @@ def rmsnorm_bwd(dout, h, rstd, weight=None, *, dh=None, dx=None, dresidual=None,
     type; h, rstd: what it returned; ``dh``: the gradient that reaches h from what
     follows (h's type), or None. Returns (dx in dout's type, dresidual in h's type,
     dweight [D] fp32, or None without a weight). Where the two types are the same
-    dresidual is dx itself. ``dx`` may be ``dout`` and ``dresidual`` may be ``dh``
-    (in place)."""
+    dresidual is dx itself. ``dx`` may be ``dout``, or a ``dh`` of its type, and
+    ``dresidual`` may be ``dh`` (in place)."""
     rows, D = _rows(dout, "dout")
     _like(h, dout, "h")
     if h.dtype != dout.dtype and h.dtype != torch.float32:
@@ -170,7 +170,7 @@ def output_gate_rmsnorm_bwd(dout, o, z, weight=None, eps=1e-6, *, do=None, dz=No
     """Gradient of output_gate_rmsnorm (kda_output_gate_rmsnorm_bwd): dout, o, z
     [..., H, dv] of one dtype; weight and eps as in the forward call. Returns
     (do, dz, dweight [dv] fp32, or None without a weight). ``do`` and ``dz`` may
-    each be one of the inputs (in place)."""
+    each be one of the inputs (in place), but not the same one."""
     _need(o, "o")
     dtype = o.dtype
     if dtype not in _DTYPES:

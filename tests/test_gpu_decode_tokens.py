@@ -253,6 +253,39 @@ def test_many_rows_of_one_head():
     assert (big["state"] == a["state"][0]).all()
 
 
+@pytest.mark.parametrize("d,H,N,K,dtype", [(64, 1, 45001, 11, BF), (64, 3, 13001, 17, F), (128, 2, 10501, 9, BF),
+                                           (128, 5, 4207, 10, F)])
+def test_many_heads_a_cta(d, H, N, K, dtype):
+    """Hundreds of heads for every CTA, most rows without tokens or with one block, some with several: outputs and
+    states bit for bit those of the same rows in small calls."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, v = n(N, K, H, d).to(dtype), n(N, K, H, d).to(dtype)
+    k = torch.nn.functional.normalize(n(N, K, H, d), dim=-1).to(dtype)
+    g, beta = n(N, K, H, d) + 3.0, torch.sigmoid(n(N, K, H))
+    state = n(N, H, d, d) * 0.1
+    counts = torch.randint(-K, K + 1, (N,), generator=gen, device="cuda").to(torch.int32)
+    counts[1000:1700] = 0  # runs of rows without tokens, longer than what a CTA looks at together takes
+    slots = torch.randperm(N, generator=gen, device="cuda").to(torch.int32)
+    slots[::50] = -1
+    before = state.clone()
+    out = decode_tokens(q, k, v, g, beta, 0.1, state, slots=slots, counts=counts, gate="logsigmoid")
+    for lo in list(range(0, N - 40, N // 23)) + [N - 40]:
+        rows = slice(lo, lo + 40)
+        at = slots[rows].long().clamp(min=0)
+        own = torch.arange(40, dtype=torch.int32, device="cuda")
+        own[slots[rows] < 0] = -1
+        part = before[at].clone()
+        want = decode_tokens(q[rows], k[rows], v[rows], g[rows], beta[rows], 0.1, part, slots=own, counts=counts[rows],
+                             gate="logsigmoid")
+        assert torch.equal(out[rows], want)
+        held = slots[rows] >= 0
+        assert torch.equal(state[at][held], part[held])
+    idle = torch.ones(N, dtype=torch.bool, device="cuda")
+    idle[slots[(slots >= 0) & (counts > 0)].long()] = False
+    assert torch.equal(state[idle], before[idle])
+
+
 def test_refusals():
     a = inputs(2, 3, 2, 64, BF)
     def call(**kw):

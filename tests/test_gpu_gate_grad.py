@@ -133,6 +133,8 @@ def test_no_tokens_streams_and_graphs():
 
 def test_refusals():
     dout, o, z, w = inputs((4, 2, 64), torch.bfloat16)
+    with pytest.raises(RuntimeError):
+        output_gate_rmsnorm_bwd(dout, o, z, w, do=o, dz=o)
     for call in (lambda: output_gate_rmsnorm_bwd(dout, o, z.float(), w), lambda: output_gate_rmsnorm_bwd(dout[:2], o, z, w),
                  lambda: output_gate_rmsnorm_bwd(dout, o, z, w[:32]), lambda: output_gate_rmsnorm_bwd(dout, o, z, dweight=w),
                  lambda: output_gate_rmsnorm_bwd(dout, o, z, w, dz=z[:1]), lambda: output_gate_rmsnorm_bwd(w, w, w, w),

@@ -125,9 +125,10 @@ def test_gradient_of_many_rows(D):
     assert all(torch.equal(a, b) for a, b in zip(again, (dx, dres, dw)))
 
 
+@pytest.mark.parametrize("D", [128, 1288, 16384])
 @pytest.mark.parametrize("dtype,rdtype", [(BF, BF), (BF, F), (F, F)])
-def test_in_place(dtype, rdtype):
-    x, res, w = inputs(50, 1288, dtype, rdtype)
+def test_in_place(dtype, rdtype, D):
+    x, res, w = inputs(50, D, dtype, rdtype)
     y, h, rstd = rmsnorm_fwd(x, w, EPS, residual=res, save_rstd=True)
     at = res.clone()
     y2, h2, _ = rmsnorm_fwd(x, w, EPS, residual=at, residual_out=at)
@@ -139,6 +140,8 @@ def test_in_place(dtype, rdtype):
     dy, dh = torch.randn_like(x), torch.randn_like(res)
     want = rmsnorm_bwd(dy, h, rstd, w, dh=dh)
     if rdtype == dtype:
+        kept = dh.clone()
+        assert all(torch.equal(a, b) for a, b in zip(rmsnorm_bwd(dy, h, rstd, w, dh=kept, dx=kept), want))
         got = rmsnorm_bwd(dy, h, rstd, w, dh=dh, dx=dy)
     else:
         got = rmsnorm_bwd(dy, h, rstd, w, dh=dh, dx=dy, dresidual=dh)
@@ -259,6 +262,9 @@ def test_refusals():
     for call in bad:
         with pytest.raises(ValueError):
             call()
+    for kw in (dict(out=x), dict(residual=x, out=x), dict(residual=x, residual_out=h.to(BF), out=x)):
+        with pytest.raises(_lib.KdaError):
+            rmsnorm_fwd(x, w, **kw)
     for D, eps in ((60, EPS), (32776, EPS), (64, 0.0)):
         with pytest.raises(_lib.KdaError):
             rmsnorm_fwd(torch.zeros(2, D, device="cuda"), None, eps)

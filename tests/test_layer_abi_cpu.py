@@ -27,13 +27,13 @@ def test_constants_of_the_header():
 
 
 def fwd(L, **kw):
-    a = dict(x=FAKE, res=None, w=None, eps=1e-6, out=FAKE, res_out=None, rstd=None, rows=4, D=12, dt=1, rdt=1)
+    a = dict(x=FAKE, res=None, w=None, eps=1e-6, out=FAKE + 65536, res_out=None, rstd=None, rows=4, D=12, dt=1, rdt=1)
     a.update(kw)
     return L.kda_rmsnorm_fwd(*a.values(), None)
 
 
 def quant(L, **kw):
-    a = dict(x=FAKE, res=None, w=None, eps=1e-6, out=FAKE, scales=FAKE, res_out=None, rows=4, D=12, block=128, dt=1, rdt=1)
+    a = dict(x=FAKE, res=None, w=None, eps=1e-6, out=FAKE + 65536, scales=FAKE, res_out=None, rows=4, D=12, block=128, dt=1, rdt=1)
     a.update(kw)
     return L.kda_rmsnorm_quant(*a.values(), None)
 
@@ -48,6 +48,10 @@ def test_norm_refusals(L, call):
                 dict(w=FAKE + 4), dict(out=FAKE + 8), dict(res=FAKE + 2, res_out=FAKE), dict(res=FAKE, res_out=FAKE + 8),
                 dict(res=FAKE, res_out=FAKE, rdt=3)):
         assert call(L, **bad) == INVALID, bad
+    far = FAKE + 4096
+    for same in (dict(out=FAKE), dict(res=far, res_out=2 * far, out=far), dict(res=far, res_out=2 * far, out=2 * far)):
+        assert call(L, **same) == INVALID, same  # out is what h is or comes from
+    assert call(L, res=far, res_out=far) == UNSUPPORTED and call(L, res=far, res_out=FAKE) == UNSUPPORTED
     assert call(L, D=8, out=None) == INVALID
     assert call(L, D=32776) == UNSUPPORTED
     assert call(L, D=8, dt=0, res=FAKE, res_out=FAKE, rdt=1) == UNSUPPORTED
@@ -68,7 +72,7 @@ def test_norm_gradient_refusals(L):
     assert bwd() == UNSUPPORTED
     for bad in (dict(D=0), dict(rows=-1), dict(rows=2 ** 31), dict(dt=5), dict(hdt=-1), dict(dout=None), dict(h=None),
                 dict(rstd=None), dict(dx=None), dict(dout=FAKE + 8), dict(h=FAKE + 8), dict(w=FAKE + 4), dict(dh=FAKE + 8),
-                dict(dx=FAKE + 8), dict(dres=FAKE + 8), dict(rstd=FAKE + 2), dict(dw=FAKE + 1)):
+                dict(dx=FAKE + 8), dict(dres=FAKE + 8), dict(dres=FAKE), dict(rstd=FAKE + 2), dict(dw=FAKE + 1)):
         assert bwd(**bad) == INVALID, bad
     assert bwd(D=8, dt=0) == UNSUPPORTED
     need = L.kda_rmsnorm_bwd_workspace_size(4, 8)
@@ -81,14 +85,14 @@ def test_norm_gradient_refusals(L):
 
 def test_gate_gradient_refusals(L):
     def bwd(**kw):
-        a = dict(dout=FAKE, o=FAKE, z=FAKE, w=FAKE, eps=1e-6, do=FAKE, dz=FAKE, dw=FAKE, tokens=4, H=2, dv=96, dt=1, ws=FAKE,
+        a = dict(dout=FAKE, o=FAKE, z=FAKE, w=FAKE, eps=1e-6, do=FAKE, dz=FAKE + 4096, dw=FAKE, tokens=4, H=2, dv=96, dt=1, ws=FAKE,
                  n=1 << 30)
         a.update(kw)
         return L.kda_output_gate_rmsnorm_bwd(*a.values(), None)
     assert bwd() == UNSUPPORTED
     for bad in (dict(tokens=-1), dict(H=0), dict(tokens=2 ** 33), dict(tokens=2 ** 62), dict(dt=2), dict(eps=0.0),
                 dict(eps=NAN), dict(dout=None), dict(o=None), dict(z=None), dict(do=None), dict(dz=None), dict(dout=FAKE + 8),
-                dict(o=FAKE + 8), dict(z=FAKE + 8), dict(do=FAKE + 8), dict(dz=FAKE + 8), dict(w=FAKE + 2), dict(dw=FAKE + 2)):
+                dict(o=FAKE + 8), dict(z=FAKE + 8), dict(do=FAKE + 8), dict(dz=FAKE + 8), dict(dz=FAKE), dict(w=FAKE + 2), dict(dw=FAKE + 2)):
         assert bwd(**bad) == INVALID, bad
     need = L.kda_output_gate_rmsnorm_bwd_workspace_size(4, 2, 64)
     assert need > 0 and L.kda_output_gate_rmsnorm_bwd_workspace_size(4, 2, 96) == 0
