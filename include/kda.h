@@ -671,11 +671,12 @@ kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const 
  *  weight     [dv] fp32 or NULL, as in the forward call
  *  dweight    [dv] fp32 (written), or NULL where it is not wanted
  *  workspace  kda_output_gate_rmsnorm_bwd_workspace_size(...) bytes, 256-byte
- *             aligned, where dweight is given; contents on entry are ignored
+ *             aligned, where dweight is given (NULL where that is 0, for few rows);
+ *             contents on entry are ignored
  * d_o may alias dout, o or z exactly, and dz likewise (not one another). Sums are
  * fp32 in a fixed order (no atomics). Sizes and alignment as the forward call.
  */
-size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv);
+size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv, kda_dtype dtype);
 kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z,
                                        const float *weight, float eps, void *d_o, void *dz,
                                        float *dweight, long long tokens, int H, int dv,
@@ -733,7 +734,7 @@ kda_status kda_rmsnorm_quant(const void *x, const void *residual, const float *w
                              int scale_block, kda_dtype dtype, kda_dtype residual_dtype,
                              cudaStream_t stream);
 
-/* Bytes of device workspace kda_rmsnorm_bwd needs for dweight. 0 for invalid sizes. */
+/* Bytes of device workspace kda_rmsnorm_bwd needs for dweight. 0 for few rows, and for invalid sizes. */
 size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D);
 
 /*
@@ -752,7 +753,8 @@ size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D);
  *             the types are the same
  *  dweight    [D] fp32 (written), or NULL where it is not wanted
  *  workspace  kda_rmsnorm_bwd_workspace_size(rows, D) bytes, 256-byte aligned,
- *             where dweight is given; contents on entry are ignored
+ *             where dweight is given (NULL where that is 0); contents on entry are
+ *             ignored
  * dx may alias dout, or a dh of its type, and dresidual dh, exactly. Sums are fp32
  * in a fixed order (no atomics). Types, sizes and alignment as the forward call.
  */

@@ -76,7 +76,7 @@ _SIGNATURES = {
                            ctypes.c_size_t, _vp], ctypes.c_int),
     "kda_decode_tokens": ([_vp] * 5 + [ctypes.c_float] + [_vp] * 4 + [ctypes.c_int] * 7 + [_vp, ctypes.c_int, _vp],
                           ctypes.c_int),
-    "kda_output_gate_rmsnorm_bwd_workspace_size": ([_ll, ctypes.c_int, ctypes.c_int], ctypes.c_size_t),
+    "kda_output_gate_rmsnorm_bwd_workspace_size": ([_ll] + [ctypes.c_int] * 3, ctypes.c_size_t),
     "kda_output_gate_rmsnorm_bwd": ([_vp] * 4 + [ctypes.c_float] + [_vp] * 3 + [_ll] + [ctypes.c_int] * 3
                                     + [_vp, ctypes.c_size_t, _vp], ctypes.c_int),
     "kda_rmsnorm_fwd": ([_vp] * 3 + [ctypes.c_float] + [_vp] * 3 + [_ll] + [ctypes.c_int] * 3 + [_vp], ctypes.c_int),

@@ -689,7 +689,8 @@ extern "C" kda_status kda_rmsnorm_quant(const void *x, const void *residual, con
 
 extern "C" size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D) {
     if (!norm_sizes_ok(rows, D) || norm_types_ok(D, KDA_DTYPE_F32, KDA_DTYPE_F32) != KDA_OK) return 0;
-    return (size_t)norm_bwd_parts(rows, D) * (size_t)D * sizeof(float);
+    const int parts = norm_bwd_parts(rows, D);
+    return parts > 1 ? (size_t)parts * (size_t)D * sizeof(float) : 0;
 }
 
 extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd, const float *weight,
@@ -705,18 +706,18 @@ extern "C" kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const flo
     if (dx && dx == dresidual) return KDA_ERR_INVALID_ARGUMENT;
     const kda_status st = norm_types_ok(D, dtype, h_dtype);
     if (st != KDA_OK) return st;
-    if (dweight && rows > 0 && (!workspace || workspace_bytes < kda_rmsnorm_bwd_workspace_size(rows, D)))
-        return KDA_ERR_WORKSPACE;
+    const size_t need = dweight ? kda_rmsnorm_bwd_workspace_size(rows, D) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
     const NormBwdArgs a = {dout, h, rstd, weight, dh, dx, dresidual, dweight, static_cast<float *>(workspace), rows, D,
                            dtype, h_dtype};
     return launch_rmsnorm_bwd(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-extern "C" size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv) {
-    if (tokens < 0 || H <= 0 || tokens >= (1LL << 34) / H || (dv != 64 && dv != 128)) return 0;
-    const long long rows = tokens * H;
-    return (size_t)(rows < kGateParts ? rows : kGateParts) * (size_t)dv * sizeof(float);
+extern "C" size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv, kda_dtype dtype) {
+    if (tokens < 0 || H <= 0 || tokens >= (1LL << 34) / H || (dv != 64 && dv != 128) || !float_type(dtype)) return 0;
+    const int parts = gate_bwd_parts(tokens * H, dv, dtype);
+    return parts > 1 ? (size_t)parts * (size_t)dv * sizeof(float) : 0;
 }
 
 extern "C" kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z, const float *weight,
@@ -732,9 +733,8 @@ extern "C" kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *
     if (!aligned4(weight) || !aligned4(dweight)) return KDA_ERR_INVALID_ARGUMENT;
     if (d_o && d_o == dz) return KDA_ERR_INVALID_ARGUMENT;
     if (dv != 64 && dv != 128) return KDA_ERR_UNSUPPORTED;
-    if (dweight && tokens > 0 &&
-        (!workspace || workspace_bytes < kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv)))
-        return KDA_ERR_WORKSPACE;
+    const size_t need = dweight ? kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv, dtype) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_WORKSPACE;
     const GateBwdArgs a = {dout, o, z, weight, eps, d_o, dz, dweight, static_cast<float *>(workspace), tokens * H, dv, dtype};
     return launch_output_gate_rmsnorm_bwd(a, stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

@@ -198,8 +198,10 @@ struct NormArgs {
 cudaError_t launch_rmsnorm(const NormArgs &a, cudaStream_t stream);
 
 // CTAs of the norms' gradients at most, each of which leaves one row of a weight gradient's parts.
+// Where it is one, that is the gradient itself.
 int norm_bwd_parts(long long rows, int D);
 constexpr int kGateParts = 1216;
+int gate_bwd_parts(long long rows, int dv, kda_dtype dtype);
 
 struct NormBwdArgs {
     const void *dy, *h;

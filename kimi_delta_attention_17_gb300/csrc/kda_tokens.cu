@@ -135,11 +135,12 @@ constexpr int token_threads = (2 * D + TokenSmem<D, InT>::kTeams * kTeam + 32 + 
 
 // Step i is in block i % 2. Its full barriers, one for each pair of warps (which need not keep step with one
 // another), are passed by the team when the block is ready and by the pair before it reads it; until the empty
-// barrier they also serve the two warps to wait for one another. Its empty barrier is passed by all of them when they have read it (and have written the state
-// behind a head's last block back into its buffer), by the team of step i + 2 before it fills it again, and by
-// the warp that moves the states. The last step is the end, which the working threads answer too; its team
-// passes the empty barriers that are left. Head h has state buffer h % 2: the empty barrier two steps before
-// its first one says that the head that had the buffer before is done with.
+// barrier they also serve the two warps to wait for one another. Its empty barrier is passed by all working
+// threads when they have read it (and have written the state behind a head's last block back into its buffer),
+// by the team of step i + 2 before it fills it again, and by the warp that moves the states. The last step is the
+// end, which the working threads answer too; its team passes the empty barriers that are left. Head h has state
+// buffer h % 2: the empty barrier two steps before its first one says that the head that had the buffer before
+// is done with.
 template <int D, typename InT>
 __global__ void __launch_bounds__(token_threads<D, InT>, D == 128 ? 1 : 2)
 decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT *__restrict__ v,

@@ -202,7 +202,7 @@ def _launch_gate_bwd(dout, o, z, weight, eps, do, dz, dweight, tokens, H, dv, st
     if weight is not None:
         if dweight is None:
             dweight = torch.empty_like(weight)
-        need = lib.kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv)
+        need = lib.kda_output_gate_rmsnorm_bwd_workspace_size(tokens, H, dv, _DTYPES[o.dtype])
         workspace = torch.empty(need, dtype=torch.uint8, device=o.device) if need else None
     status = lib.kda_output_gate_rmsnorm_bwd(
         dout.data_ptr(), o.data_ptr(), z.data_ptr(), _ptr(weight), eps, do.data_ptr(), dz.data_ptr(), _ptr(dweight),

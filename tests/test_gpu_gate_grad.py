@@ -41,7 +41,7 @@ def check(dout, o, z, w, got):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("dv", [64, 128])
-@pytest.mark.parametrize("lead", [(1, 1), (7, 3), (2, 5, 4), (77, 32), (20011, 1)])
+@pytest.mark.parametrize("lead", [(1, 1), (7, 3), (2, 5, 4), (5, 51), (1, 257), (77, 32), (20011, 1)])
 def test_gradient(lead, dv, dtype):
     for weighted in (True, False):
         dout, o, z, w = inputs(lead + (dv,), dtype, seed=dv)

@@ -75,11 +75,13 @@ def test_norm_gradient_refusals(L):
                 dict(dx=FAKE + 8), dict(dres=FAKE + 8), dict(dres=FAKE), dict(rstd=FAKE + 2), dict(dw=FAKE + 1)):
         assert bwd(**bad) == INVALID, bad
     assert bwd(D=8, dt=0) == UNSUPPORTED
-    need = L.kda_rmsnorm_bwd_workspace_size(4, 8)
-    assert need == 4 * 8 * 4 and L.kda_rmsnorm_bwd_workspace_size(10 ** 6, 8) < 10 ** 6
+    need = L.kda_rmsnorm_bwd_workspace_size(4000, 8)
+    assert 0 < need < 10 ** 6 and L.kda_rmsnorm_bwd_workspace_size(2 ** 31 - 1, 8) < 10 ** 6
+    assert L.kda_rmsnorm_bwd_workspace_size(4, 8) == 0 and L.kda_rmsnorm_bwd_workspace_size(0, 8) == 0
     for D in (0, 12, 32776):
         assert L.kda_rmsnorm_bwd_workspace_size(4, D) == 0
-    assert bwd(D=8, ws=None) == WORKSPACE and bwd(D=8, n=need - 1) == WORKSPACE and bwd(D=8, ws=FAKE + 64) == WORKSPACE
+    many = dict(D=8, rows=4000)
+    assert bwd(**many, ws=None) == WORKSPACE and bwd(**many, n=need - 1) == WORKSPACE and bwd(D=8, ws=FAKE + 64) == WORKSPACE
     assert bwd(D=8, rows=0, dw=None, dout=None, h=None, rstd=None, dx=None, ws=None) == OK
 
 
@@ -94,10 +96,12 @@ def test_gate_gradient_refusals(L):
                 dict(eps=NAN), dict(dout=None), dict(o=None), dict(z=None), dict(do=None), dict(dz=None), dict(dout=FAKE + 8),
                 dict(o=FAKE + 8), dict(z=FAKE + 8), dict(do=FAKE + 8), dict(dz=FAKE + 8), dict(dz=FAKE), dict(w=FAKE + 2), dict(dw=FAKE + 2)):
         assert bwd(**bad) == INVALID, bad
-    need = L.kda_output_gate_rmsnorm_bwd_workspace_size(4, 2, 64)
-    assert need > 0 and L.kda_output_gate_rmsnorm_bwd_workspace_size(4, 2, 96) == 0
-    assert L.kda_output_gate_rmsnorm_bwd_workspace_size(2 ** 62, 2, 64) == 0
-    assert bwd(dv=64, ws=None) == WORKSPACE and bwd(dv=64, n=need - 1) == WORKSPACE and bwd(dv=64, ws=FAKE + 128) == WORKSPACE
+    size = L.kda_output_gate_rmsnorm_bwd_workspace_size
+    need = size(4000, 2, 64, 1)
+    assert need > 0 and size(4000, 2, 96, 1) == 0 and size(4000, 2, 64, 2) == 0 and size(2 ** 62, 2, 64, 1) == 0
+    assert size(4, 2, 64, 1) == 0 and size(2 ** 32, 2, 64, 1) < 10 ** 6
+    many = dict(dv=64, tokens=4000)
+    assert bwd(**many, ws=None) == WORKSPACE and bwd(**many, n=need - 1) == WORKSPACE and bwd(dv=64, ws=FAKE + 128) == WORKSPACE
     assert bwd(dv=64, tokens=0, dw=None, dout=None, o=None, z=None, do=None, dz=None, ws=None) == OK
 
 
