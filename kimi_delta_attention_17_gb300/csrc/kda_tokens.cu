@@ -296,8 +296,11 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
         for (int step = team;; step += kTeams) {
             auto &bl = sm.block[step & 1];
             auto &in = sm.in[team];
-            if (step >= 2) tc::bar_sync(kBarEmpty + (step & 1), kEmpty);
+            const auto empty_wait = [step] {
+                if (step >= 2) tc::bar_sync(kBarEmpty + (step & 1), kEmpty);
+            };
             if (task.place < 0) {
+                empty_wait();
                 if (first_end) {
                     if (tid == 0) bl.task = task;
                     pass_full(step);
@@ -310,10 +313,6 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
             tc::cp_async_wait_all();
             team_wait();  // this block's inputs are here
             const int some = min(kBlock, task.count - task.t0);
-            if (tid == 0) {
-                bl.task = task;
-                sm.ring[(step + 2) & 3] = second;
-            }
             if (pro.decay == KDA_DECAY_CHANNEL) {
                 for (int p = tid; p < some * (D / 4); p += kTeam) {
                     float4 *at = reinterpret_cast<float4 *>(&in.a[p / (D / 4)][p % (D / 4) * 4]);
@@ -325,7 +324,13 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
                     in.a[p / D][p % D] =
                         pro.decay == KDA_DECAY_NONE ? 1.f : decay_factor(g[task.row + (long long)(p / D) * H], pro);
             }
+            // Up to here the block that is filled may still be read: of 10000 cycles with 8 tokens half are over by then.
+            empty_wait();
             team_wait();
+            if (tid == 0) {
+                bl.task = task;
+                sm.ring[(step + 2) & 3] = second;
+            }
             // The vectors of the reads by k and by q and of the update, two channels a lane; then tokens j in turn:
             // A_tj, H_tj for t >= j (A_jj is |k_j|^2), and |q_j|^2.
             constexpr int kUnits = D / 64;  // warps' worth of channels
