@@ -103,42 +103,50 @@ def _launch_compact(pool, live, new_slot, count, slots, layers, nbytes, stream):
 _STORE_TYPES = {torch.int8: _lib.STORE["int8"], torch.float8_e4m3fn: _lib.STORE["e4m3"]}
 
 
-def _store_call(entry, pool, store, scales, src, dst, slot_dim, stream):
+def _store_call(launch, pool, store, scales, src, dst, slot_dim, stream):
     """Checks the arguments of state_quantize and state_dequantize and launches one."""
-    layers, slots, nbytes = _pool(pool, "pool", slot_dim)
-    if pool.dtype != torch.float32:
-        raise ValueError("pool must be float32")
-    _, store_slots, values = _pool(store, "store", slot_dim)
+    _need(pool, "pool", torch.float32)
+    _need(store, "store")
+    _need(scales, "scales", torch.float32)
+    _need(src, "src", torch.int32, 1)
+    _need(dst, "dst", torch.int32, 1)
+    if slot_dim != 0 and slot_dim != 1:
+        raise ValueError("slot_dim must be 0 (a pool [P, ...]) or 1 ([L, P, ...])")
     if store.dtype not in _STORE_TYPES:
         raise ValueError("store must be int8 or float8_e4m3fn")
-    shape, kept = pool.shape, store.shape
-    if shape[:slot_dim] != kept[:slot_dim] or shape[slot_dim + 1:] != kept[slot_dim + 1:]:
+    shape, kept, factors, lead = pool.shape, store.shape, scales.shape, slot_dim + 1
+    if len(shape) <= lead or kept[lead:] != shape[lead:] or (slot_dim and kept[0] != shape[0]) or len(kept) != len(shape):
         raise ValueError("store must have the pool's layers and slot shape")
-    _need(scales, "scales", torch.float32)
-    if scales.dim() <= slot_dim or scales.shape[:slot_dim + 1] != kept[:slot_dim + 1]:
+    if factors[:lead] != kept[:lead]:
         raise ValueError("scales must have the store's layers and slots")
-    per = scales.numel() // (layers * store_slots)
+    size, layers = pool.numel(), shape[0] if slot_dim else 1
+    if size == 0 or store.numel() == 0:
+        raise ValueError("pool and store must not be empty")
+    values = size // (layers * shape[slot_dim])
+    per = scales.numel() // (layers * kept[slot_dim])
     block = values // per if per and values % per == 0 else 0
     if block not in (32, 64, 128):
         raise ValueError("scales must hold one value for each 32, 64 or 128 of a slot's")
-    _need(src, "src", torch.int32, 1)
-    _need(dst, "dst", torch.int32, 1)
     if src.shape != dst.shape:
         raise ValueError("src and dst must have the same length")
-    _on_stream(_launch_store, ("pool", "store", "scales", "src", "dst"), (pool, store, scales, src, dst), stream,
-               entry, pool, slots, store, scales, store_slots, src, dst, layers, values, block)
+    _on_stream(launch, ("pool", "store", "scales", "src", "dst"), (pool, store, scales, src, dst), stream,
+               pool, shape[slot_dim], store, scales, kept[slot_dim], src, dst, layers, values, block)
 
 
-def _launch_store(entry, pool, slots, store, scales, store_slots, src, dst, layers, values, block, stream):
-    lists = (src.data_ptr(), dst.data_ptr(), src.shape[0], layers, values, block, _STORE_TYPES[store.dtype], stream)
-    if entry == "kda_state_quantize":
-        status = _lib.lib().kda_state_quantize(pool.data_ptr(), slots, store.data_ptr(), scales.data_ptr(), store_slots,
-                                               *lists)
-    else:
-        status = _lib.lib().kda_state_dequantize(store.data_ptr(), scales.data_ptr(), store_slots, pool.data_ptr(),
-                                                 slots, *lists)
+def _launch_quantize(pool, slots, store, scales, store_slots, src, dst, layers, values, block, stream):
+    status = _lib.lib().kda_state_quantize(
+        pool.data_ptr(), slots, store.data_ptr(), scales.data_ptr(), store_slots, src.data_ptr(), dst.data_ptr(),
+        src.shape[0], layers, values, block, _STORE_TYPES[store.dtype], stream)
     if status:
-        _lib.check(entry, status)
+        _lib.check("kda_state_quantize", status)
+
+
+def _launch_dequantize(pool, slots, store, scales, store_slots, src, dst, layers, values, block, stream):
+    status = _lib.lib().kda_state_dequantize(
+        store.data_ptr(), scales.data_ptr(), store_slots, pool.data_ptr(), slots, src.data_ptr(), dst.data_ptr(),
+        src.shape[0], layers, values, block, _STORE_TYPES[store.dtype], stream)
+    if status:
+        _lib.check("kda_state_dequantize", status)
 
 
 def state_quantize(pool, src, store, scales, dst, *, slot_dim=0, stream=None):
@@ -153,7 +161,7 @@ def state_quantize(pool, src, store, scales, dst, *, slot_dim=0, stream=None):
     ``src``, ``dst`` int32 [n] on the device, n <= 4096, as in state_copy: src -1
     stores zeros, entries out of range are skipped, of entries that name one
     destination the last holds. Returns (store, scales)."""
-    _store_call("kda_state_quantize", pool, store, scales, src, dst, slot_dim, stream)
+    _store_call(_launch_quantize, pool, store, scales, src, dst, slot_dim, stream)
     return store, scales
 
 
@@ -162,5 +170,5 @@ def state_dequantize(store, scales, src, pool, dst, *, slot_dim=0, stream=None):
     (kda_state_dequantize): the way back of state_quantize, with its arguments.
     One source in several entries resumes several samples of a prefix. Returns
     ``pool``."""
-    _store_call("kda_state_dequantize", pool, store, scales, src, dst, slot_dim, stream)
+    _store_call(_launch_dequantize, pool, store, scales, src, dst, slot_dim, stream)
     return pool
