@@ -331,91 +331,110 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
                 bl.task = task;
                 sm.ring[(step + 2) & 3] = second;
             }
-            // The vectors of the reads by k and by q and of the update, two channels a lane; then tokens j in turn:
-            // A_tj, H_tj for t >= j (A_jj is |k_j|^2), and |q_j|^2.
-            constexpr int kUnits = D / 64;  // warps' worth of channels
-            for (int unit = kTeam / 32 - 1 - warp; unit < 3 * kUnits; unit += kTeam / 32) {
-                const int role = unit / kUnits, c = (unit % kUnits * 32 + lane) * 2;
-                float G[2] = {1.f, 1.f};
-                if (role < 2) {
-                    const float f = role ? scale : 1.f;
-                    const InT(*from)[D] = role ? in.q : in.k;
-                    for (int i = 0; i < some; ++i) {  // what the places behind hold stays in their columns of the product
-                        float a[2], z[2];
-                        some_of<2>(&in.a[i][c], a);
-                        some_of<2>(&from[i][c], z);
-                        G[0] *= a[0];
-                        G[1] *= a[1];
-                        const float w0 = G[0] * (f * z[0]), w1 = G[1] * (f * z[1]), h0 = tf32_hi(w0), h1 = tf32_hi(w1);
-                        *reinterpret_cast<float4 *>(&bl.read[role][i][2 * c]) = make_float4(h0, h1, w0 - h0, w1 - h1);
-                    }
-                } else {
+            // For a block of at most kN tokens, without branches between them; places behind the last token hold what
+            // they hold, and their results are not used.
+            const auto prepare = [&](auto n) {
+                constexpr int kN = decltype(n)::value;
+                // The vectors of the reads by k and by q and of the update, two channels a lane.
+                constexpr int kUnits = D / 64;  // warps' worth of channels
+                for (int unit = kTeam / 32 - 1 - warp; unit < 3 * kUnits; unit += kTeam / 32) {
+                    const int role = unit / kUnits, c = (unit % kUnits * 32 + lane) * 2;
+                    const InT(*from)[D] = role == 1 ? in.q : in.k;
+                    float a[kN][2], z[kN][2], G[2] = {1.f, 1.f};
 #pragma unroll
-                    for (int i = kBlock - 1; i >= 0; --i) {
-                        float a[2] = {1.f, 1.f}, z[2] = {0.f, 0.f};
-                        if (i < some) {
-                            some_of<2>(&in.a[i][c], a);
-                            some_of<2>(&in.k[i][c], z);
+                    for (int i = 0; i < kN; ++i) {
+                        some_of<2>(&in.a[i][c], a[i]);
+                        some_of<2>(&from[i][c], z[i]);
+                    }
+                    if (role < 2) {
+                        const float f = role ? scale : 1.f;
+#pragma unroll
+                        for (int i = 0; i < kN; ++i) {
+                            G[0] *= a[i][0];
+                            G[1] *= a[i][1];
+                            const float w0 = G[0] * (f * z[i][0]), w1 = G[1] * (f * z[i][1]), h0 = tf32_hi(w0), h1 = tf32_hi(w1);
+                            *reinterpret_cast<float4 *>(&bl.read[role][i][2 * c]) = make_float4(h0, h1, w0 - h0, w1 - h1);
                         }
-                        const float w0 = G[0] * z[0], w1 = G[1] * z[1], h0 = tf32_hi(w0), h1 = tf32_hi(w1);
-                        *reinterpret_cast<float4 *>(&bl.write[i][2 * c]) = make_float4(h0, w0 - h0, h1, w1 - h1);
-                        G[0] *= a[0];
-                        G[1] *= a[1];
+                    } else {  // the update's product sums over all of its places: zeros behind the last token
+#pragma unroll
+                        for (int i = kBlock - 1; i >= 0; --i) {
+                            float w0 = 0.f, w1 = 0.f;
+                            if (i < kN && i < some) {
+                                w0 = G[0] * z[i][0];
+                                w1 = G[1] * z[i][1];
+                                G[0] *= a[i][0];
+                                G[1] *= a[i][1];
+                            }
+                            const float h0 = tf32_hi(w0), h1 = tf32_hi(w1);
+                            *reinterpret_cast<float4 *>(&bl.write[i][2 * c]) = make_float4(h0, w0 - h0, h1, w1 - h1);
+                        }
+                        *reinterpret_cast<float2 *>(&bl.total[c]) = make_float2(G[0], G[1]);
                     }
-                    *reinterpret_cast<float2 *>(&bl.total[c]) = make_float2(G[0], G[1]);
                 }
-            }
-            for (int j = warp; j < some; j += kTeam / 32) {
-                constexpr int kC = D / 32;  // channels a lane
+                // A_tj, H_tj for t >= j (A_jj is |k_j|^2), and |q_j|^2: a warp takes every third token j, all of them at
+                // once where its registers hold their sums (64 channels, two CTAs an SM: one after another).
+                constexpr int kC = D / 32, kMost = (kN + kTeam / 32 - 1) / (kTeam / 32), kJ = D == 128 ? kMost : 1;
                 const int c = kC * lane;
-                float acc[2 * kBlock], w[kC], qss = 0.f;
-                some_of<kC>(&in.k[j][c], w);
+#pragma unroll 1
+                for (int j0 = warp; j0 < kN; j0 += kJ * (kTeam / 32)) {
+                    float acc[kJ][2 * kN], w[kJ][kC], qss[kJ];
 #pragma unroll
-                for (int t = 0; t < kBlock; ++t) {
-                    acc[t] = acc[kBlock + t] = 0.f;
-                    if (t < j || t >= some) continue;
-                    float kt[kC], qt[kC];
-                    some_of<kC>(&in.k[t][c], kt);
-                    some_of<kC>(&in.q[t][c], qt);
-                    if (t > j) {
-                        float a[kC];
+                    for (int i = 0; i < kJ; ++i) {
+                        qss[i] = 0.f;
+                        some_of<kC>(&in.k[min(j0 + i * (kTeam / 32), kN - 1)][c], w[i]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < kN; ++t) {
+                        float a[kC], kt[kC], qt[kC];
                         some_of<kC>(&in.a[t][c], a);
+                        some_of<kC>(&in.k[t][c], kt);
+                        some_of<kC>(&in.q[t][c], qt);
 #pragma unroll
-                        for (int m = 0; m < kC; ++m) w[m] *= a[m];
-                    } else {
+                        for (int i = 0; i < kJ; ++i) {
+                            const int j = j0 + i * (kTeam / 32);
+                            acc[i][t] = acc[i][kN + t] = 0.f;
 #pragma unroll
-                        for (int m = 0; m < kC; ++m) qss += qt[m] * qt[m];
+                            for (int m = 0; m < kC; ++m) {
+                                if (t > j) w[i][m] *= a[m];
+                                if (t == j) qss[i] += qt[m] * qt[m];
+                                acc[i][t] += kt[m] * w[i][m];
+                                acc[i][kN + t] += qt[m] * w[i][m];
+                            }
+                        }
                     }
 #pragma unroll
-                    for (int m = 0; m < kC; ++m) {
-                        acc[t] += kt[m] * w[m];
-                        acc[kBlock + t] += qt[m] * w[m];
+                    for (int i = 0; i < kJ; ++i) {
+                        // 2 kN sums over the warp: every step halves the values a lane holds.
+#pragma unroll
+                        for (int m = 16, left = kN; m > 0; m >>= 1, left >>= 1) {
+                            const bool up = lane & m;
+                            if (left == 0) acc[i][0] += __shfl_xor_sync(0xffffffffu, acc[i][0], m);
+#pragma unroll
+                            for (int x = 0; x < left; ++x) {
+                                const float keep = up ? acc[i][x + left] : acc[i][x], send = up ? acc[i][x] : acc[i][x + left];
+                                acc[i][x] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                            }
+                        }
+                        // The sum for token t (of H in the upper half of the warp) is in 16 / kN lanes.
+                        const int j = j0 + i * (kTeam / 32), t = lane % 16 / (16 / kN);
+                        if (j < kN && lane % (16 / kN) == 0)
+                            (lane < 16 ? bl.A : bl.Hm)[t][j] = lane < 16 ? acc[i][0] : scale * acc[i][0];
+                        float rk = 1.f, rq = 1.f;
+                        if (pro.l2norm) {
+                            rk = rsqrtf(__shfl_sync(0xffffffffu, acc[i][0], min(j, kN - 1) * (16 / kN)) + kL2Eps);
+                            rq = rsqrtf(lanes_sum<32>(qss[i]) + kL2Eps);
+                        }
+                        if (j < kN && lane == 0) {
+                            bl.rk[j] = rk;
+                            bl.rq[j] = rq;
+                        }
                     }
                 }
-                // Sixteen sums over the warp: every step halves the values a lane holds.
-#pragma unroll
-                for (int m = 16, left = kBlock; left > 0; m >>= 1, left >>= 1) {
-                    const bool up = lane & m;
-#pragma unroll
-                    for (int i = 0; i < left; ++i) {
-                        const float keep = up ? acc[i + left] : acc[i], send = up ? acc[i] : acc[i + left];
-                        acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                    }
-                }
-                const float sum = acc[0] + __shfl_xor_sync(0xffffffffu, acc[0], 1);
-                const int t = lane >> 1 & 7;
-                if ((lane & 1) == 0 && t >= j) (lane < 16 ? bl.A : bl.Hm)[t][j] = lane < 16 ? sum : scale * sum;
-                if (pro.l2norm) {
-                    qss = lanes_sum<32>(qss);
-                    const float kss = __shfl_sync(0xffffffffu, sum, 2 * j);
-                    if (lane == 0) {
-                        bl.rk[j] = rsqrtf(kss + kL2Eps);
-                        bl.rq[j] = rsqrtf(qss + kL2Eps);
-                    }
-                } else if (lane == 0) {
-                    bl.rk[j] = bl.rq[j] = 1.f;
-                }
-            }
+            };
+            if (some <= kBlock / 2)
+                prepare(std::integral_constant<int, kBlock / 2>{});
+            else
+                prepare(std::integral_constant<int, kBlock>{});
             pass_full(step);
             team_wait();  // the inputs are read no more
             first_end = kTeams == 1 || next.place >= 0;
