@@ -27,10 +27,11 @@
 // head, and everything behind them in its queue waited; row by row, 128 bulk copies of 512 bytes took 8000
 // cycles to issue.)
 //
-// 256 rows of up to 8 tokens each, 32 heads of 128: 190-198 us (5.3 TB/s), of 8 verified 183, of 4 committed 186,
-// of one 177 (the single step takes 183). HBM bounds the few-token calls; with 8 tokens a head's chain of phases
-// does (read 2500 cycles, solve 1000, outputs 700, update 1700, state in and out 1800; two working warps share a
-// sub-partition), at 40 % of the issue slots.
+// 256 rows, 32 heads of 128: up to 8 tokens each committed 185-190 us (5.4 TB/s), 8 each 214, 4 each 184, one 179 (the
+// single step takes 183); 8 verified 160, 4 verified 112, one 102. HBM bounds the calls of few tokens that write
+// states (1.07 GB: 158 us); with more, a head's chain of phases does (cycles with 8 tokens: copy waited for and
+// state into registers 1400, read 2600, solve 800, outputs 700, update 1700, state out 500), and with 8 the
+// teams that prepare come close to it; 40 % of the issue slots are busy.
 #include <cuda.h>  // CUtensorMap (the encoder is fetched at run time; no libcuda link)
 
 #include "kda_rows.cuh"
