@@ -167,6 +167,33 @@ def test_a_row_that_is_not_finite_touches_no_other():
     assert torch.isnan(out[1]).all() and torch.isfinite(a["state"][0]).all() and torch.isfinite(a["state"][3]).all()
 
 
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, BF), (128, F)])
+def test_what_lies_behind_the_counts_is_not_read(d, dtype):
+    """NaN and infinities in the tokens behind a row's count, and in rows without a slot, touch nothing."""
+    counts, slots = [3, 0, 9, 17, 8, 5, 1], [6, 5, 4, 3, 2, -1, 0]
+    a = inputs(7, 17, 2, d, dtype, gate="logsigmoid", l2norm=True)
+    how = dict(slots=i32(slots), counts=i32(counts), gate="logsigmoid", l2norm_qk=True)
+    clean = a["state"].clone()
+    want = decode_tokens(a["q"], a["k"], a["v"], a["g"], a["beta"], 0.1, clean, **how)
+    for n, (c, s) in enumerate(zip(counts, slots)):
+        for x, name in enumerate(("q", "k", "v", "g", "beta")):
+            a[name][n, 0 if s < 0 else c:] = (float("nan"), float("inf"), -float("inf"))[(n + x) % 3]
+    for _ in range(2):  # the second time over what the first left in shared memory
+        state = a["state"].clone()
+        out = decode_tokens(a["q"], a["k"], a["v"], a["g"], a["beta"], 0.1, state, **how)
+        assert torch.equal(out, want) and torch.equal(state, clean)
+
+
+def test_rows_may_share_a_state_that_is_not_written():
+    a = inputs(4, 5, 3, 64, BF, P=3)
+    before = a["state"].clone()
+    out = decode_tokens(a["q"], a["k"], a["v"], a["g"], a["beta"], 0.1, a["state"], slots=i32([1, 1, 2, 1]), write_state=False)
+    for n, at in enumerate((1, 1, 2, 1)):
+        row = [a[x][n:n + 1] for x in ("q", "k", "v", "g", "beta")]
+        assert torch.equal(out[n:n + 1], decode_tokens(*row, 0.1, before[at:at + 1].clone()))
+    assert torch.equal(a["state"], before)
+
+
 def test_no_rows_no_tokens_given_outputs():
     a = inputs(2, 3, 2, 64, BF)
     before = a["state"].clone()
