@@ -57,8 +57,9 @@ rmsnorm_bwd_kernel(const X *dy, const Hh *__restrict__ h, const float *__restric
     const int warp = threadIdx.x >> 5, warps = threads >> 5;
     const int groups = D / 8;
     // Up to 16 values a thread the weights, u and n stay in registers. Wider rows form them again after the sum:
-    // from the row as it was loaded (16 bits), or from the L2 cache.
-    constexpr bool kKeep = kGroups <= 2, kRaw = !kKeep && sizeof(Hh) == 2 && kThreads <= 512;
+    // from the row as it was loaded where that fits (24 values a thread, or 32 with an h of 16 bits), or from the
+    // L2 cache.
+    constexpr bool kKeep = kGroups <= 2, kRaw = !kKeep && (sizeof(Hh) == 2 || kGroups == 3) && kThreads <= 512;
     constexpr bool kNext = kKeep && sizeof(Hh) == 2;
     float wv[kKeep ? kGroups : 1][8], dw[kGroups][8];
     auto weights = [&](int i, float *v) {
@@ -225,6 +226,7 @@ cudaError_t launch_bwd_t(const NormBwdArgs &a, cudaStream_t stream) {
     if (s.groups == 1) return launch_bwd_k<X, Hh, 0, 1, 1, 512, 2>(a, s.threads, stream);
     if (s.groups == 2 && s.threads <= 256) return launch_bwd_k<X, Hh, 0, 2, 1, 256, 2>(a, s.threads, stream);
     if (s.groups == 2) return launch_bwd_k<X, Hh, 0, 2, 1, 512, 1>(a, s.threads, stream);
+    if (s.groups == 3) return launch_bwd_k<X, Hh, 0, 3, 1, 512, 1>(a, s.threads, stream);
     if (s.threads <= 512) return launch_bwd_k<X, Hh, 0, 4, 1, 512, 1>(a, s.threads, stream);
     return launch_bwd_k<X, Hh, 0, 4, 1, 1024, 1>(a, s.threads, stream);
 }

@@ -80,8 +80,9 @@ inline RowThreads row_threads(int D, bool backward) {
     const auto warps = [D](int groups) { return ((D / 8 + groups - 1) / groups + 31) / 32; };
     // Two groups a thread; four where two would take more than 512 threads. The backward pass takes one where that
     // leaves fewer lanes idle (60000 x 1032, bf16: 94 us, and 111 with two; the forward pass 85 and 87, but with an
-    // 8-bit output 102 and 85).
-    const int groups = D > 8192 ? 4 : backward && D <= 4096 && warps(1) < 2 * warps(2) ? 1 : 2;
+    // 8-bit output 102 and 85), and three up to the width where that takes 512 threads, which leaves registers for
+    // fp32 rows (4000 x 12288, fp32: 149 us, and 179 with four; 4000 x 8200: 104 and 152).
+    const int groups = D > 8192 ? (backward && D <= 12288 ? 3 : 4) : backward && D <= 4096 && warps(1) < 2 * warps(2) ? 1 : 2;
     return {32 * warps(groups), groups};
 }
 

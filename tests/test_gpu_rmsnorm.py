@@ -125,6 +125,26 @@ def test_gradient_of_many_rows(D):
     assert all(torch.equal(a, b) for a, b in zip(again, (dx, dres, dw)))
 
 
+@pytest.mark.parametrize("dtype,rdtype", [(BF, None), (BF, BF), (BF, F), (F, F)])
+@pytest.mark.parametrize("D", [8200, 10240, 12280, 12288, 12296])
+def test_gradient_of_wide_rows(D, dtype, rdtype):
+    """Several rows a CTA at the widths where a thread takes three groups and where it no longer does, also in place."""
+    rows = 317
+    x, res, w = inputs(rows, D, dtype, rdtype)
+    gen = torch.Generator().manual_seed(6)
+    dy = torch.randn(rows, D, generator=gen).to(dtype).cuda()
+    _, h, rstd = rmsnorm_fwd(x, w, EPS, residual=res, save_rstd=True)
+    dh = None if res is None else torch.randn(rows, D, generator=gen).to(h.dtype).cuda()
+    dx, dres, dw = rmsnorm_bwd(dy, h, rstd, w, dh=dh)
+    r = ref.norm_grad(f64(dy), f64(h), f64(w), EPS, None if dh is None else f64(dh))
+    close(dx, r["dx"], r["tol_dx"] + half_step(r["dx"], dtype == BF), "dx")
+    close(dres, r["dx"], r["tol_dx"] + half_step(r["dx"], h.dtype == BF), "dresidual")
+    close(dw, r["dw"], r["tol_dw"] + half_step(r["dw"], False), "dweight")
+    kw = {} if dh is None or h.dtype == dtype else {"dresidual": dh}
+    got = rmsnorm_bwd(dy, h, rstd, w, dh=dh, dx=dy, **kw)
+    assert got[0] is dy and all(torch.equal(a, b) for a, b in zip(got, (dx, dres, dw)))
+
+
 @pytest.mark.parametrize("D", [128, 1288, 16384])
 @pytest.mark.parametrize("dtype,rdtype", [(BF, BF), (BF, F), (F, F)])
 def test_in_place(dtype, rdtype, D):
