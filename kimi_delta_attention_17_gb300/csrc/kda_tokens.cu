@@ -142,6 +142,16 @@ constexpr int token_threads = (2 * D + TokenSmem<D, InT>::kTeams * kTeam + 32 + 
 // end, which the working threads answer too; its team passes the empty barriers that are left. Head h has state
 // buffer h % 2: the empty barrier two steps before its first one says that the head that had the buffer before
 // is done with.
+//
+// The teams look for heads in windows of kWindow pairs, which both fill: at a window's end a team waits in the
+// window barrier until the other one is there too. With two teams, one that has passed step t on looks as far as
+// step t + 4, so where it waits the other one comes by when it has passed step t + 1 on at the latest. For that
+// block (t + 1) % 2 has to be empty: step t - 1, which the other one passed on itself, has to be worked off, and the
+// mover, which the waiting team met in step t - 2's empty barrier, has to be there. None of it waits for the team
+// that waits. The begin barrier, in which the mover waits for the ring's first two tasks, is passed by both teams
+// when they have looked at steps 0 and 1. (Behind the look at steps 2 and 3, the first of which only team 0 takes
+// and the second only team 1, three blocks before a window's end made team 1 wait in one barrier and team 0 in the
+// other, for ever.)
 template <int D, typename InT>
 __global__ void __launch_bounds__(token_threads<D, InT>, D == 128 ? 1 : 2)
 decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT *__restrict__ v,
@@ -286,13 +296,13 @@ decode_tokens_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const
         if (tid == 0 && team == 0) sm.ring[0] = task;
         next = advance(task);
         if (tid == 0 && team == 0) sm.ring[1] = next;
+        tc::bar_sync(kBarBegin, kPrep + 32);  // before either team looks further than the other (above)
         if (team == 1) {
             first_end = task.place >= 0;
             task = next;
             next = advance(task);
         }
         second = advance(next);
-        tc::bar_sync(kBarBegin, kPrep + 32);
         fetch(task, team);
         for (int step = team;; step += kTeams) {
             auto &bl = sm.block[step & 1];
