@@ -756,7 +756,8 @@ size_t kda_rmsnorm_bwd_workspace_size(long long rows, int D);
  *             where dweight is given (NULL where that is 0); contents on entry are
  *             ignored
  * dx may alias dout, or a dh of its type, and dresidual dh, exactly. Sums are fp32
- * in a fixed order (no atomics). Types, sizes and alignment as the forward call.
+ * in a fixed order (no atomics). Types, sizes and alignment as the forward call
+ * (dweight 4-byte).
  */
 kda_status kda_rmsnorm_bwd(const void *dout, const void *h, const float *rstd,
                            const float *weight, const void *dh, void *dx, void *dresidual,

@@ -50,7 +50,7 @@ rmsnorm_bwd_kernel(const X *dy, const Hh *__restrict__ h, const float *__restric
                    const float *__restrict__ w, const Hh *dh, X *dx, Hh *dres,  // may be in place
                    float *__restrict__ part, long long rows, int D) {
     using S = BwdShape<kTpr>;
-    extern __shared__ float rows_dw[];  // [S::rows][D], where a CTA has several rows
+    extern __shared__ __align__(16) float rows_dw[];  // [S::rows][D], where a CTA has several rows
     __shared__ __align__(16) float sums[2][32];
     const int threads = kTpr ? S::threads : blockDim.x;
     const int tpr = kTpr ? kTpr : threads, lane = kTpr ? threadIdx.x % kTpr : threadIdx.x, sub = kTpr ? threadIdx.x / tpr : 0;
@@ -195,10 +195,19 @@ rmsnorm_bwd_kernel(const X *dy, const Hh *__restrict__ h, const float *__restric
             part[(size_t)blockIdx.x * D + c] = t;
         }
     } else {
+        // Parts are 16-byte aligned; the weight's gradient itself, which one CTA writes, may begin at any float.
+        const bool wide = (reinterpret_cast<uintptr_t>(part) & 15u) == 0;
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             const int c = lane + i * tpr;
-            if (c < groups) store8(part + (size_t)blockIdx.x * D + 8 * c, dw[i]);
+            if (c >= groups) continue;
+            float *to = part + (size_t)blockIdx.x * D + 8 * c;
+            if (wide) {
+                store8(to, dw[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) to[j] = dw[i][j];
+            }
         }
     }
 }
