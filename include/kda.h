@@ -651,8 +651,11 @@ kda_status kda_state_compact(void *pool, int num_slots, const uint8_t *live, int
  *  K          0 .. KDA_DECODE_TOKENS_MAX
  * Results equal the single steps' up to fp32 rounding: products are formed from
  * operands split in two, to some 2^-22 of their magnitudes; a state that keeps
- * its values (decays of 1, nothing written) keeps them exactly. No workspace;
- * options and errors as kda_decode_step_opt.
+ * its values (decays of 1, nothing written) keeps them exactly. A value of the
+ * state, of k, of scale q or of what is written that reaches
+ * 2^128 (1 - 2^-12) = 3.4019e38 in magnitude counts as not finite, as infinities
+ * do: its row and head may become NaN. No workspace; options and errors as
+ * kda_decode_step_opt.
  */
 kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const float *g,
                              const float *beta, float scale, float *state, const int32_t *slots,

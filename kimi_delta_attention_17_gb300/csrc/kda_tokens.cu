@@ -51,7 +51,10 @@ __device__ __forceinline__ void tma_store_3d(const void *map, int x, int y, int 
                  : "memory");
 }
 
-// The nearest value of 11 bits. (NaN may come out as a zero: what is left of it, x - hi, is NaN still.)
+// The nearest value of 11 bits. (NaN may come out as a zero: what is left of it, x - hi, is NaN still. From
+// 2^128 (1 - 2^-12) on it is infinite, and what is left is no number: the call's documented range ends there.
+// Limited to the largest finite value, one instruction more for each of a state's values, 256 rows of 8 tokens, 32
+// heads of 128, took 229 us for 216 committed and 184 for 163 verified; of 64 channels 111 for 100.)
 __device__ __forceinline__ float tf32_hi(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
 
 // c += a b: a 16 x 8 (row m = lane / 4 and m + 8; column k = lane % 4 and k + 4), b 8 x 8 (row k, column
