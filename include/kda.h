@@ -677,7 +677,9 @@ kda_status kda_decode_tokens(const void *q, const void *k, const void *v, const 
  *             aligned, where dweight is given (NULL where that is 0, for few rows);
  *             contents on entry are ignored
  * d_o may alias dout, o or z exactly, and dz likewise (not one another). Sums are
- * fp32 in a fixed order (no atomics). Sizes and alignment as the forward call.
+ * fp32 in a fixed order (no atomics); s, as in the forward call, is off by up to
+ * (10 + 2.4 |z|) 2^-24 of itself in either dtype. Sizes and alignment as the
+ * forward call.
  */
 size_t kda_output_gate_rmsnorm_bwd_workspace_size(long long tokens, int H, int dv, kda_dtype dtype);
 kda_status kda_output_gate_rmsnorm_bwd(const void *dout, const void *o, const void *z,

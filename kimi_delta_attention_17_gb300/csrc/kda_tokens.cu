@@ -27,11 +27,13 @@
 // head, and everything behind them in its queue waited; row by row, 128 bulk copies of 512 bytes took 8000
 // cycles to issue.)
 //
-// 256 rows, 32 heads of 128: up to 8 tokens each committed 185-190 us (5.4 TB/s), 8 each 214, 4 each 184, one 179 (the
-// single step takes 183); 8 verified 160, 4 verified 112, one 102. HBM bounds the calls of few tokens that write
-// states (1.07 GB: 158 us); with more, a head's chain of phases does (cycles with 8 tokens: copy waited for and
-// state into registers 1400, read 2600, solve 800, outputs 700, update 1700, state out 500), and with 8 the
-// teams that prepare come close to it; 40 % of the issue slots are busy.
+// 256 rows, 32 heads of 128: up to 8 tokens each committed 185-187 us (5.4 TB/s), 8 each 216, 4 each 186, one 181 (the
+// single step takes 182), 16 each 389; 8 verified 162, 4 verified 113, one 103, 16 verified 328. HBM bounds the calls
+// of few tokens that write states (1.07 GB: 158 us); with more, a head's chain of phases does (cycles with 8 tokens:
+// copy waited for and state into registers 1400, read 2600, solve 800, outputs 700, update 1700, state out 500), and
+// with 8 the teams that prepare come close to it; 40 % of the issue slots are busy. With fp32 inputs, which leave
+// shared memory for one team, it bounds the call: 8 committed 291, verified 219. 32 heads of 64: 8 committed 100,
+// verified 83, one committed 66; a head's phases are no shorter there, for a quarter of the state.
 #include <cuda.h>  // CUtensorMap (the encoder is fetched at run time; no libcuda link)
 
 #include "kda_rows.cuh"
